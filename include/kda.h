@@ -13,7 +13,7 @@
  * on q.  A NaN log-decay is treated as the floor (fmaxf semantics).  Precondition: log_alpha <= 0 (a
  * decay in (0, 1], i.e. forgetting).  The bf16 chunk path relies on it for the in-tile bound e^80.09 of
  * the floor section; a positive log-decay is outside the contract and can give inf or NaN there with
- * no status code.
+ * no status code.  (kda_lin_* and kda_pages_* below are described with their declarations.)
  *
  * Conventions for every entry point:
  *  - Pointers are DEVICE pointers unless the argument says "host".  The caller owns every buffer; the
@@ -35,7 +35,7 @@
  *    wait that ran out) are recorded in the per-device status word and read with
  *    kda_get_device_status; the kernels never trap.
  *  - Supported sizes: dk, dv in {64, 128} for KDA_F32; dk = 128 and dv in {64, 128} for KDA_BF16 and
- *    for kda_chunk_fwd_mxfp8; dk, dv in {64, 128} for the decode calls of every type.
+ *    for kda_chunk_fwd_mxfp8; dk, dv in {64, 128} for the decode calls and kda_lin_* of every type.
  */
 #ifndef KDA_H_
 #define KDA_H_
@@ -63,7 +63,8 @@ typedef enum {
     KDA_ERR_CUDA = -4,         /* a CUDA runtime call failed (launch, symbol, attribute) */
     KDA_ERR_TIMEOUT = -5,      /* device: a bounded wait inside a kernel ran out */
     KDA_ERR_WORKSPACE = -6,    /* workspace too small for even one chunk window */
-    KDA_ERR_DEVICE_INPUT = -7  /* device: cu_seqlens / seg_cu / ckpt_cu inconsistent */
+    KDA_ERR_DEVICE_INPUT = -7, /* device: cu_seqlens / seg_cu / ckpt_cu, a slot or a page table inconsistent */
+    KDA_ERR_NO_PAGES = -8      /* device: not enough free pages */
 } kda_status_t;
 
 /* KDA_MXFP8: MXFP8 q, k, v (kda_chunk_fwd_mxfp8 only; for the workspace queries it sizes like KDA_BF16). */
@@ -250,6 +251,112 @@ KDA_API kda_status_t kda_segment_compose(const float* transitions, const float* 
                                  const int32_t* seg_cu, const float* init,
                                  int n_seqs, int n_segs, int H, int dk, int dv,
                                  float* start_states, float* end_states, kda_stream_t stream);
+
+/*
+ * Decayed linear attention: the state of KDA without the delta rule, and with one decay per head instead of
+ * one per key channel.  Per (sequence, head):
+ *
+ *     S_t = a_t S_{t-1} + k_t v_t^T,        o_t = S_t^T q_t,        a_t = exp(log_alpha_t).
+ *
+ * There is no scale on q and no floor under the decay: a_t may be any value in [0, 1].  log_alpha below
+ * -120, minus infinity and NaN among it, is a decay of 0 (exp(-120) is 0 in fp32): the state is forgotten
+ * before token t is added.  log_alpha > 0 is outside the contract.
+ *
+ *   q, k       [T_tot, Hqk, dk]; H must be a multiple of Hqk, and head h reads q and k of head h Hqk / H
+ *   v, o       [T_tot, H, dv]
+ *   log_alpha  fp32, [T_tot, H] when la_per_token is 1, or [H] (a constant of each head) when it is 0
+ *   states     [*, H, dk, dv] fp32
+ *   dtype      KDA_BF16 or KDA_F32 for q, k, v and o; dk, dv in {64, 128} for both
+ * Non-finite q, k or v of a token makes outputs of the same (sequence, head) non-finite from the start of
+ * the token's chunk of KDA_CHUNK tokens on; other sequences and heads, and earlier chunks, are untouched.
+ *
+ * kda_lin_chunk_fwd: the chunked form over a packed batch; cu_seqlens, initial_state, final_state,
+ *   ckpt_stride, checkpoints and ckpt_cu as in kda_chunk_fwd.  Sequences of length 0 are allowed (the
+ *   final state is the initial one).  The states are accumulated in fp32 from exact products for both
+ *   types; a bf16 call rounds the scores inside a chunk and the state that q is multiplied with once each to
+ *   bf16 on the way to o.  q, k, v, o, states and checkpoints are 16-byte aligned, the workspace (at least
+ *   kda_lin_chunk_fwd_workspace_bytes, contents ignored) 256-byte aligned.  Results do not depend on what
+ *   else is in the batch except through the split of long sequences into segments, which depends on
+ *   (total_tokens, n_seqs, H) and changes the order of fp32 sums only.
+ *
+ * kda_lin_recurrent_step: one token for each of n rows, states in place.  slots (device int32, or NULL
+ *   for slots[i] = i) names the state of row i among n_states; entry i is slots[i * slot_stride], so that a
+ *   column of a page table can be passed.  A row with a negative slot is idle: nothing of it is read, its
+ *   rows of o stay as they were.  A slot outside n_states, or one that two rows name, is an error: those
+ *   rows are left out (state and o as they were) and the status word becomes KDA_ERR_DEVICE_INPUT.
+ *   state is 16-byte aligned; the per-token inputs need element alignment only.
+ */
+KDA_API size_t kda_lin_chunk_fwd_workspace_bytes(int64_t total_tokens, int n_seqs, int H, int dk, int dv,
+                                         kda_dtype_t dtype);
+KDA_API kda_status_t kda_lin_chunk_fwd(const void* q, const void* k, const void* v, const float* log_alpha,
+                               int la_per_token, const float* initial_state,
+                               const int32_t* cu_seqlens, int n_seqs, int64_t total_tokens,
+                               int Hqk, int H, int dk, int dv, kda_dtype_t dtype, int ckpt_stride,
+                               void* o, float* final_state, float* checkpoints, const int32_t* ckpt_cu,
+                               void* workspace, size_t ws_bytes, kda_stream_t stream);
+KDA_API kda_status_t kda_lin_recurrent_step(float* state, int64_t n_states, const int32_t* slots, int slot_stride,
+                                    const void* q, const void* k, const void* v, const float* log_alpha,
+                                    int la_per_token, int n, int Hqk, int H, int dk, int dv, kda_dtype_t dtype,
+                                    void* o, kda_stream_t stream);
+
+/*
+ * Pages of a cache on the device.  A pool is n_planes arrays of n_pages pages of page_bytes each, one
+ * after another ([n_planes, n_pages, page_bytes]; a plane is a layer, or the keys or values of one); a page
+ * holds a recurrent state or some tokens.  The prefix directory below decides on the host which checkpoint
+ * lives in which slot; these calls move the pages themselves and keep a running batch's tables, on the
+ * device and in stream order, so that they can be part of a captured graph.  Pools are 16-byte aligned and
+ * page_bytes is a multiple of 16.
+ *
+ * kda_pages_copy: page src_pages[i] of src (n_src pages) to page dst_pages[i] of dst (n_dst pages), for i
+ *   in 0..n-1; a NULL table means i itself.  One source may be copied to many destinations.  An entry with
+ *   a negative page is left out, and so is a copy of a page to itself (dst == src).  dst and src may be the
+ *   same pool, but not overlap in any other way (KDA_ERR_ARG).  Copies that depend on each other are
+ *   errors: a destination named twice, or (in one pool) a page that one copy reads and another writes.
+ *   All copies of such a page, and any with a page out of range, are left out, the others are made, and the
+ *   status word becomes KDA_ERR_DEVICE_INPUT.
+ *
+ * The bookkeeping of a batch (device int32, owned and initialised by the caller: all refs and counts 0 for
+ * an empty cache):
+ *   refs   [n_pages]            how many table entries name the page; 0 = free
+ *   table  [n_rows, max_pages]  the pages of each row, in order; entries behind a row's count mean nothing
+ *   counts [n_rows]             pages of each row
+ *
+ * kda_pages_fork: opens n rows.  Row children[i] continues row parents[i]: its first n_shared[i] pages are
+ *   the parent's own (refs + 1), the parent's other pages are copied to new pages, and n_fresh[i] further
+ *   new pages (n_fresh NULL: none) follow, zeroed when zero_fresh is set and otherwise as they were.
+ *   parents[i] = -1 opens a row of fresh pages alone; parents[i] = children[i] appends the fresh pages to
+ *   that row.  New pages are the free ones in ascending order, given out in order of i and of the page's
+ *   place in its row.  A child must be empty (unless it is its own parent) and may be opened once in a call;
+ *   a row that a call opens or extends is no other entry's parent in it.  If an entry breaks these rules, is
+ *   out of range or does not fit max_pages, the whole call changes nothing and the status word becomes
+ *   KDA_ERR_DEVICE_INPUT; if the free pages do not suffice, it changes nothing and the status word becomes
+ *   KDA_ERR_NO_PAGES.
+ * kda_pages_free: the rows' pages lose a reference each and their counts become 0 (tables and page
+ *   contents stay as they were).  Naming a row twice frees it once.  A row out of range is left out, a page
+ *   out of range or without references is too, and the status word becomes KDA_ERR_DEVICE_INPUT.
+ * kda_pages_compact: moves pages so that the n_live pages in use become pages 0..n_live-1: the k-th page in
+ *   use behind the first n_live fills the k-th free page among them, the others stay.  refs and the tables
+ *   follow; remap [n_pages] receives each page's new number (-1 for free pages) and n_live (device, one
+ *   int32, or NULL) the count.  A table entry out of range, or naming a free page, stays as it was and the
+ *   status word becomes KDA_ERR_DEVICE_INPUT.
+ * The workspaces are 256-byte aligned device scratch of at least the bytes the queries give.
+ */
+KDA_API kda_status_t kda_pages_copy(void* dst, int64_t n_dst, const void* src, int64_t n_src,
+                            const int32_t* dst_pages, const int32_t* src_pages, int n, size_t page_bytes,
+                            kda_stream_t stream);
+KDA_API size_t kda_pages_fork_workspace_bytes(int n, int max_pages);
+KDA_API kda_status_t kda_pages_fork(void* pool, int n_planes, int n_pages, size_t page_bytes,
+                            int32_t* refs, int32_t* table, int32_t* counts, int n_rows, int max_pages,
+                            const int32_t* parents, const int32_t* children, const int32_t* n_shared,
+                            const int32_t* n_fresh, int n, int zero_fresh,
+                            void* workspace, size_t ws_bytes, kda_stream_t stream);
+KDA_API kda_status_t kda_pages_free(int32_t* refs, int n_pages, const int32_t* table, int32_t* counts, int n_rows,
+                            int max_pages, const int32_t* rows, int n, kda_stream_t stream);
+KDA_API size_t kda_pages_compact_workspace_bytes(int n_pages);
+KDA_API kda_status_t kda_pages_compact(void* pool, int n_planes, int n_pages, size_t page_bytes,
+                               int32_t* refs, int32_t* table, const int32_t* counts, int n_rows, int max_pages,
+                               int32_t* remap, int32_t* n_live, void* workspace, size_t ws_bytes,
+                               kda_stream_t stream);
 
 /*
  * Prefix reuse bookkeeping (orkas.ai "Kimi K3 architecture" post, section "비용은 서빙 스택에서

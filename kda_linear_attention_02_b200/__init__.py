@@ -23,6 +23,8 @@ __all__ = [
     "kda_prefix_cache_destroy", "kda_prefix_cache_lookup", "kda_prefix_cache_plan", "kda_prefix_cache_insert",
     "kda_prefix_cache_commit", "kda_prefix_cache_abort", "kda_prefix_cache_release", "kda_prefix_cache_stats",
     "KDA_PREFIX_NO_SLOT", "KDA_PREFIX_STORED",
+    "kda_lin_chunk_fwd_workspace_bytes", "kda_lin_chunk_fwd", "kda_lin_recurrent_step", "kda_pages_copy",
+    "kda_pages_fork", "kda_pages_free", "kda_pages_compact",
 ]
 
 KDA_BF16 = 0
@@ -100,6 +102,25 @@ def _load():
     L.kda_prefix_cache_stats.argtypes = [vp, i64p, ctypes.POINTER(i32)]
     L.kda_segment_compose.restype = i32
     L.kda_segment_compose.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]
+    L.kda_lin_chunk_fwd_workspace_bytes.restype = sz
+    L.kda_lin_chunk_fwd_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32]
+    L.kda_lin_chunk_fwd.restype = i32
+    L.kda_lin_chunk_fwd.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, i64, i32, i32, i32, i32, i32, i32,
+                                    vp, vp, vp, vp, vp, sz, vp]
+    L.kda_lin_recurrent_step.restype = i32
+    L.kda_lin_recurrent_step.argtypes = [vp, i64, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp]
+    L.kda_pages_copy.restype = i32
+    L.kda_pages_copy.argtypes = [vp, i64, vp, i64, vp, vp, i32, sz, vp]
+    L.kda_pages_fork_workspace_bytes.restype = sz
+    L.kda_pages_fork_workspace_bytes.argtypes = [i32, i32]
+    L.kda_pages_fork.restype = i32
+    L.kda_pages_fork.argtypes = [vp, i32, i32, sz, vp, vp, vp, i32, i32, vp, vp, vp, vp, i32, i32, vp, sz, vp]
+    L.kda_pages_free.restype = i32
+    L.kda_pages_free.argtypes = [vp, i32, vp, vp, i32, i32, vp, i32, vp]
+    L.kda_pages_compact_workspace_bytes.restype = sz
+    L.kda_pages_compact_workspace_bytes.argtypes = [i32]
+    L.kda_pages_compact.restype = i32
+    L.kda_pages_compact.argtypes = [vp, i32, i32, sz, vp, vp, vp, i32, i32, vp, vp, vp, sz, vp]
     L.kda_ckpt_offsets.restype = i32
     L.kda_ckpt_offsets.argtypes = [vp, i32, i32, vp]
     L.kda_get_device_status.restype = i32
@@ -314,6 +335,233 @@ def kda_chunk_fwd_noalloc(q, k, v, log_alpha, beta, initial_state, cu_seqlens, o
                                        _stream(stream))
     _check(st, "kda_chunk_fwd_noalloc")
     return o
+
+
+def kda_lin_chunk_fwd_workspace_bytes(total_tokens, n_seqs, H, dk, dv, dtype=KDA_BF16) -> int:
+    return int(_load().kda_lin_chunk_fwd_workspace_bytes(int(total_tokens), int(n_seqs), int(H), int(dk), int(dv),
+                                                         int(dtype)))
+
+
+def _launch_on(t: torch.Tensor, name: str, stream):
+    """(device guard, stream) of a call whose tensors live where `t` does: the given stream, else the current
+    one of that device, which the guard makes the current device for the launch."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"stream: expected device {t.device}, got {stream.device}")
+    return torch.cuda.device(t.device), torch.cuda.current_stream(t.device) if stream is None else stream
+
+
+def _scratch(nbytes, dev, stream):
+    """uint8 scratch from torch's allocator that belongs to the stream the kernels run on: its memory is reused
+    in that stream's order."""
+    with torch.cuda.stream(stream):
+        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
+
+
+def _log_alpha(log_alpha, n, H, dev):
+    """Checks log_alpha and tells whether it is per token ([n, H]) or a constant of each head ([H])."""
+    per_token = log_alpha is None or log_alpha.dim() != 1
+    _need(log_alpha, "log_alpha", (n, H) if per_token else (H,), torch.float32, dev)
+    return int(per_token)
+
+
+def kda_lin_chunk_fwd(q, k, v, log_alpha, initial_state, cu_seqlens, o, final_state=None, *, ckpt_stride=0,
+                      checkpoints=None, ckpt_cu=None, workspace=None, stream=None):
+    """Chunked decayed linear attention over a packed batch (C: kda_lin_chunk_fwd).
+
+    S_t = a_t S_{t-1} + k_t v_t^T, o_t = S_t^T q_t, a_t = exp(log_alpha_t), one decay per head.  q, k
+    [T,Hqk,dk] (bf16 or fp32; H a multiple of Hqk); v, o [T,H,dv]; log_alpha fp32 [T,H], or [H] for a constant
+    of each head; cu_seqlens int32 [N+1] (device); initial_state / final_state [N,H,dk,dv] fp32 or None;
+    checkpoints, ckpt_cu and workspace as in kda_chunk_fwd.  Outputs are written in place.
+    """
+    _need(q, "q")
+    dev = q.device
+    if q.dim() != 3 or v is None or v.dim() != 3 or cu_seqlens is None:
+        raise ValueError("q, v must be [T, heads, channels] and cu_seqlens [N + 1]")
+    T, Hqk, dk = q.shape
+    H, dv = v.shape[1], v.shape[2]
+    dt = _dtype_code(q)
+    n = cu_seqlens.numel() - 1
+    _need(k, "k", (T, Hqk, dk), q.dtype, dev)
+    _need(v, "v", (T, H, dv), q.dtype, dev)
+    _need(o, "o", (T, H, dv), q.dtype, dev)
+    per_token = _log_alpha(log_alpha, T, H, dev)
+    _need(cu_seqlens, "cu_seqlens", (n + 1,), torch.int32, dev)
+    _opt(initial_state, "initial_state", (n, H, dk, dv), torch.float32, dev)
+    _opt(final_state, "final_state", (n, H, dk, dv), torch.float32, dev)
+    if ckpt_stride:
+        _need(checkpoints, "checkpoints", None, torch.float32, dev)
+        if checkpoints.dim() != 4 or tuple(checkpoints.shape[1:]) != (H, dk, dv):
+            raise ValueError("checkpoints must be [n_ckpt, H, dk, dv]")
+        _need(ckpt_cu, "ckpt_cu", (n + 1,), torch.int32, dev)
+    guard, stream = _launch_on(q, "q", stream)
+    if workspace is None:
+        workspace = _scratch(kda_lin_chunk_fwd_workspace_bytes(T, n, H, dk, dv, dt), dev, stream)
+    _need(workspace, "workspace", None, torch.uint8, dev)
+    ck = bool(ckpt_stride) and checkpoints.numel() > 0
+    with guard:
+        st = _load().kda_lin_chunk_fwd(_p(q), _p(k), _p(v), _p(log_alpha), per_token, _p(initial_state), _p(cu_seqlens),
+                                       n, T, Hqk, H, dk, dv, dt, int(ckpt_stride) if ck else 0, _p(o), _p(final_state),
+                                       _p(checkpoints if ck else None), _p(ckpt_cu if ck else None), _p(workspace),
+                                       workspace.numel(), ctypes.c_void_p(stream.cuda_stream))
+    _check(st, "kda_lin_chunk_fwd")
+    return o
+
+
+def kda_lin_recurrent_step(state, q, k, v, log_alpha, o, *, slots=None, stream=None):
+    """One token of decayed linear attention for each row, states in place (C: kda_lin_recurrent_step).
+
+    state [n_states,H,dk,dv] fp32; q, k [n,Hqk,dk]; v, o [n,H,dv] (bf16 or fp32); log_alpha fp32 [n,H] or [H].
+    slots: int32 [n] (device; a strided 1-D view such as a column of a page table is fine), the state of each
+    row; a negative slot marks an idle row, which is left alone.  None: row i uses state i.
+    """
+    _need(state, "state", None, torch.float32)
+    dev = state.device
+    if state.dim() != 4 or q is None or q.dim() != 3:
+        raise ValueError("state must be [n_states, H, dk, dv] and q [n, Hqk, dk]")
+    n_states, H, dk, dv = state.shape
+    n, Hqk = q.shape[0], q.shape[1]
+    dt = _dtype_code(q)
+    _need(q, "q", (n, Hqk, dk), q.dtype, dev)
+    _need(k, "k", (n, Hqk, dk), q.dtype, dev)
+    _need(v, "v", (n, H, dv), q.dtype, dev)
+    _need(o, "o", (n, H, dv), q.dtype, dev)
+    per_token = _log_alpha(log_alpha, n, H, dev)
+    stride = 1
+    if slots is not None:
+        if slots.dim() != 1 or slots.shape[0] != n or slots.dtype != torch.int32 or slots.device != dev:
+            raise ValueError(f"slots must be int32 [{n}] on {dev}")
+        stride = slots.stride(0) if n > 1 else 1
+        if stride <= 0:
+            raise ValueError("slots: entries must not share memory")
+    elif n > n_states:
+        raise ValueError(f"{n} rows need as many states, got {n_states}")
+    guard, stream = _launch_on(state, "state", stream)
+    with guard:
+        st = _load().kda_lin_recurrent_step(_p(state), n_states, _p(slots), stride, _p(q), _p(k), _p(v), _p(log_alpha),
+                                            per_token, n, Hqk, H, dk, dv, dt, _p(o),
+                                            ctypes.c_void_p(stream.cuda_stream))
+    _check(st, "kda_lin_recurrent_step")
+    return o
+
+
+def _page_bytes(t, name, first):
+    _need(t, name)
+    if t.dim() < first + 1 or t.numel() == 0:
+        raise ValueError(f"{name} must be {'[n_planes, n_pages, ...]' if first == 2 else '[n_pages, ...]'} and not empty")
+    n = t.element_size()
+    for x in t.shape[first:]:
+        n *= x
+    if n % 16:
+        raise ValueError(f"{name}: a page has {n} bytes, not a multiple of 16")
+    return n
+
+
+def kda_pages_copy(dst, src, dst_pages=None, src_pages=None, *, stream=None):
+    """dst[dst_pages[i]] = src[src_pages[i]] for every i (C: kda_pages_copy).
+
+    dst [n_dst, ...] and src [n_src, ...]: contiguous, with the same dtype and page shape; they may be the same
+    tensor.  dst_pages, src_pages: int32 (device), one of them may be None for 0, 1, ...; a negative entry leaves
+    that copy out, and one source may go to many destinations.
+    """
+    nb = _page_bytes(dst, "dst", 1)
+    _need(src, "src", (src.shape[0], *dst.shape[1:]) if src is not None and src.dim() else None, dst.dtype, dst.device)
+    lens = [t.shape[0] for t in (dst_pages, src_pages) if t is not None and t.dim() == 1]
+    n = lens[0] if lens else src.shape[0]
+    _opt(dst_pages, "dst_pages", (n,), torch.int32, dst.device)
+    _opt(src_pages, "src_pages", (n,), torch.int32, dst.device)
+    guard, stream = _launch_on(dst, "dst", stream)
+    with guard:
+        st = _load().kda_pages_copy(_p(dst), dst.shape[0], _p(src), src.shape[0], _p(dst_pages), _p(src_pages), n, nb,
+                                    ctypes.c_void_p(stream.cuda_stream))
+    _check(st, "kda_pages_copy")
+    return dst
+
+
+def _book(refs, table, counts, dev):
+    if refs is None or table is None or refs.dim() != 1 or table.dim() != 2:
+        raise ValueError("refs must be [n_pages] and table [n_rows, max_pages]")
+    _need(refs, "refs", None, torch.int32, dev)
+    _need(table, "table", None, torch.int32, dev)
+    _need(counts, "counts", (table.shape[0],), torch.int32, dev)
+
+
+def kda_pages_fork(pool, refs, table, counts, parents, children, n_shared=None, n_fresh=None, *, zero_fresh=False,
+                   workspace=None, stream=None):
+    """Opens rows that continue others (C: kda_pages_fork).
+
+    pool [n_planes, n_pages, ...]; refs [n_pages], table [n_rows, max_pages], counts [n_rows]: int32, the
+    bookkeeping that the call updates.  Per entry i (int32 [n], device): row children[i] gets the first
+    n_shared[i] pages of row parents[i] (None: none), copies of its other pages, and n_fresh[i] new ones
+    (None: none), zeroed with zero_fresh.  parents[i] = -1: fresh pages alone; parents[i] = children[i]: the
+    row is extended.  A call that cannot be carried out changes nothing; kda_get_device_status tells why.
+    """
+    nb = _page_bytes(pool, "pool", 2)
+    dev = pool.device
+    _book(refs, table, counts, dev)
+    if refs.shape[0] != pool.shape[1]:
+        raise ValueError(f"refs: expected {pool.shape[1]} pages, got {refs.shape[0]}")
+    _need(parents, "parents", None, torch.int32, dev)
+    n = parents.numel()
+    guard, stream = _launch_on(pool, "pool", stream)
+    if n_shared is None:
+        with torch.cuda.stream(stream):
+            n_shared = torch.zeros(n, dtype=torch.int32, device=dev)
+    for x, name in ((parents, "parents"), (children, "children"), (n_shared, "n_shared")):
+        _need(x, name, (n,), torch.int32, dev)
+    _opt(n_fresh, "n_fresh", (n,), torch.int32, dev)
+    rows, most = table.shape
+    if workspace is None:
+        workspace = _scratch(_load().kda_pages_fork_workspace_bytes(n, most), dev, stream)
+    _need(workspace, "workspace", None, torch.uint8, dev)
+    with guard:
+        st = _load().kda_pages_fork(_p(pool), pool.shape[0], pool.shape[1], nb, _p(refs), _p(table), _p(counts), rows, most,
+                                    _p(parents), _p(children), _p(n_shared), _p(n_fresh), n, int(bool(zero_fresh)),
+                                    _p(workspace), workspace.numel(), ctypes.c_void_p(stream.cuda_stream))
+    _check(st, "kda_pages_fork")
+
+
+def kda_pages_free(refs, table, counts, rows, *, stream=None):
+    """Frees the rows: each of their pages loses a reference, their counts become 0 (C: kda_pages_free)."""
+    _need(refs, "refs")
+    dev = refs.device
+    _book(refs, table, counts, dev)
+    _need(rows, "rows", (rows.numel(),) if rows is not None else None, torch.int32, dev)
+    guard, stream = _launch_on(refs, "refs", stream)
+    with guard:
+        st = _load().kda_pages_free(_p(refs), refs.shape[0], _p(table), _p(counts), table.shape[0], table.shape[1],
+                                    _p(rows), rows.shape[0], ctypes.c_void_p(stream.cuda_stream))
+    _check(st, "kda_pages_free")
+
+
+def kda_pages_compact(pool, refs, table, counts, *, remap=None, n_live=None, workspace=None, stream=None):
+    """Moves the pages in use to the front of the pool; refs and table follow (C: kda_pages_compact).
+
+    Arguments as in kda_pages_fork.  remap int32 [n_pages] receives each page's new number (-1: free; allocated
+    here when None), n_live int32 [1] the number of pages in use.  Returns remap.
+    """
+    nb = _page_bytes(pool, "pool", 2)
+    dev = pool.device
+    _book(refs, table, counts, dev)
+    n_pages = pool.shape[1]
+    if refs.shape[0] != n_pages:
+        raise ValueError(f"refs: expected {n_pages} pages, got {refs.shape[0]}")
+    guard, stream = _launch_on(pool, "pool", stream)
+    if remap is None:
+        with torch.cuda.stream(stream):
+            remap = torch.empty(n_pages, dtype=torch.int32, device=dev)
+    _need(remap, "remap", (n_pages,), torch.int32, dev)
+    _opt(n_live, "n_live", (1,), torch.int32, dev)
+    if workspace is None:
+        workspace = _scratch(_load().kda_pages_compact_workspace_bytes(n_pages), dev, stream)
+    _need(workspace, "workspace", None, torch.uint8, dev)
+    with guard:
+        st = _load().kda_pages_compact(_p(pool), pool.shape[0], n_pages, nb, _p(refs), _p(table), _p(counts), table.shape[0],
+                                       table.shape[1], _p(remap), _p(n_live), _p(workspace), workspace.numel(),
+                                       ctypes.c_void_p(stream.cuda_stream))
+    _check(st, "kda_pages_compact")
+    return remap
 
 
 def kda_recurrent_step(state, q, k, v, log_alpha, beta, o, *, stream=None):

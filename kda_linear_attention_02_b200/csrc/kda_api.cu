@@ -137,14 +137,14 @@ long long chunk_upper_bound(int64_t total_tokens, int n_seqs) {
 
 kda_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
+}  // namespace
+
 // Device address of the current device's status word.
-int* status_ptr() {
+int* kda::status_ptr() {
     int* p = nullptr;
     if (cudaGetSymbolAddress(reinterpret_cast<void**>(&p), g_status) != cudaSuccess) return nullptr;
     return p;
 }
-
-}  // namespace
 
 extern "C" {
 
@@ -160,6 +160,7 @@ const char* kda_status_string(kda_status_t st) {
         case KDA_ERR_TIMEOUT: return "KDA_ERR_TIMEOUT";
         case KDA_ERR_WORKSPACE: return "KDA_ERR_WORKSPACE";
         case KDA_ERR_DEVICE_INPUT: return "KDA_ERR_DEVICE_INPUT";
+        case KDA_ERR_NO_PAGES: return "KDA_ERR_NO_PAGES";
     }
     return "KDA_ERR_UNKNOWN";
 }

@@ -12,6 +12,9 @@ namespace kda {
 // The driver's tensor-map encoder (looked up once; nullptr when the driver lacks it) (kda_chunk_bf16.cu).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
+// Device address of the current device's status word, or null (kda_api.cu).
+int* status_ptr();
+
 // Decode step (kda_decode.cu).
 cudaError_t launch_decode(float* state, const void* q, const void* k, const void* v, const float* la,
                           const float* beta, void* o, int nh, int dk, int dv, bool bf16, cudaStream_t s);

@@ -1,0 +1,265 @@
+// kda_lin.cu -- decayed linear attention, host side and bookkeeping: argument checks, the split of the batch
+// into segments, and the pass that joins the segments' states.
+//
+// A sequence is walked chunk by chunk, and the state passes from chunk to chunk, so one (sequence, head)
+// occupies one SM at a time.  A batch with few long sequences would leave SMs idle; its sequences are cut
+// into segments.  Since a segment acts on the state it starts from by one factor alone,
+//
+//     S_end = e^{sum of log_alpha} S_start + Z,
+//
+// every segment with a successor is walked once from a zero state for its Z (reading k and v only), the
+// starts of all segments follow from a short scan, and the segments are then walked in full side by side.
+#include <algorithm>
+
+#include "kda_device.cuh"
+#include "kda_lin.h"
+
+namespace kda {
+
+namespace {
+
+// Splits the sequences into segments of seg_len tokens and validates cu_seqlens (cu[0] = 0, non-decreasing,
+// cu[N] = total); a bad table gives no items, so that the kernels behind do nothing.  When all items fit one
+// block they are ordered by length, longest first: blocks start in that order, and a long sequence that
+// started last would run on alone at the end.
+__global__ void __launch_bounds__(1024) lin_index_kernel(const int32_t* __restrict__ cu, int n_seqs, int total,
+                                                         int seg_len, int max_items, LinHead* head, LinItem* items,
+                                                         int2* multi, int* status) {
+    __shared__ long long warp_sums[32];
+    __shared__ int lens[1024];
+    __shared__ int s_multi;
+    grid_dependency_wait();
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    if (t == 0) s_multi = 0;
+    bool bad = t == 0 && (cu[0] != 0 || cu[n_seqs] != total);
+    for (int i = t; i < n_seqs; i += 1024) bad |= cu[i + 1] < cu[i];
+    if (__syncthreads_or(bad)) {
+        if (t == 0) {
+            *head = LinHead{0, 0, {0, 0}};
+            set_status(status, KDA_ERR_DEVICE_INPUT);
+        }
+        return;
+    }
+    long long carry = 0;   // items in the low half, boundaries in the high half
+    for (int base = 0; base < n_seqs; base += 1024) {
+        const int i = base + t;
+        int t0 = 0, len = 0, ns = 0;
+        if (i < n_seqs) {
+            t0 = cu[i];
+            len = cu[i + 1] - t0;
+            ns = len > seg_len ? (len - 1) / seg_len + 1 : 1;
+        }
+        const long long c = ns ? (static_cast<long long>(ns - 1) << 32) | ns : 0;
+        long long x = c;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        if (lane == 31) warp_sums[w] = x;
+        __syncthreads();
+        if (w == 0) {
+            long long s = warp_sums[lane];
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, s, off);
+                if (lane >= off) s += y;
+            }
+            warp_sums[lane] = s;
+        }
+        __syncthreads();
+        const long long first = carry + x - c + (w ? warp_sums[w - 1] : 0);
+        const int item0 = static_cast<int>(first & 0xffffffff), z0 = static_cast<int>(first >> 32);
+        for (int s = 0; s < ns; ++s)
+            items[item0 + s] = LinItem{i, s, ns, t0 + s * seg_len, min(seg_len, len - s * seg_len), s * seg_len, z0, 0};
+        if (ns > 1) multi[atomicAdd(&s_multi, 1)] = make_int2(z0, ns);   // their order has no effect
+        carry += warp_sums[31];
+        __syncthreads();
+    }
+    const int n_items = static_cast<int>(carry & 0xffffffff);
+    if (t == 0) *head = LinHead{n_items, s_multi, {0, 0}};
+    if (n_items <= 1024) {
+        LinItem it{};
+        if (t < n_items) {
+            it = items[t];
+            lens[t] = it.n;
+        }
+        __syncthreads();
+        if (t < n_items) {
+            int rank = 0;
+            for (int j = 0; j < n_items; ++j) rank += lens[j] > it.n || (lens[j] == it.n && j < t);
+            items[rank] = it;
+        }
+    }
+}
+
+// Starts of the segments: z[s] holds the end state of segment s from a zero state (segment 0: from the
+// sequence's own start), and becomes the state at the start of segment s + 1.  A thread carries four
+// elements of one state through the boundaries of its sequence.
+__global__ void __launch_bounds__(256) lin_join_kernel(const LinHead* __restrict__ head, const int2* __restrict__ multi,
+                                                       float* __restrict__ z, const float* __restrict__ zdecay, int H,
+                                                       int elems) {
+    grid_dependency_wait();
+    const int e4 = (blockIdx.x * 256 + threadIdx.x) * 4, h = e4 / elems;
+    if (h >= H) return;
+    for (int m = blockIdx.y; m < head->n_multi; m += gridDim.y) {
+        const int z0 = multi[m].x, nb = multi[m].y - 1;
+        float4* p = reinterpret_cast<float4*>(z + static_cast<size_t>(z0) * H * elems + e4);
+        const size_t pitch = static_cast<size_t>(H) * elems / 4;
+        const float* d = zdecay + static_cast<size_t>(z0) * H + h;
+        float4 x = p[0];
+#pragma unroll 4
+        for (int s = 1; s < nb; ++s) {
+            const float a = d[static_cast<size_t>(s) * H];
+            const float4 y = p[s * pitch];
+            x = make_float4(fmaf(a, x.x, y.x), fmaf(a, x.y, y.y), fmaf(a, x.z, y.z), fmaf(a, x.w, y.w));
+            p[s * pitch] = x;
+        }
+    }
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_chained(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+bool dims_ok(int dk, int dv) { return (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }
+
+// Tokens per segment.  No segment is longer than a fair share of the batch's (token, head) pairs over the
+// SMs, plus a quarter; none is shorter than kMinSeg, below which the extra pass costs more than it gives.
+constexpr int kSms = 148, kMinSeg = 1024;
+int segment_tokens(int64_t total_tokens, int H) {
+    const int64_t share = (total_tokens * H * 5 + kSms * 4 - 1) / (kSms * 4);
+    const int64_t len = std::max<int64_t>(kMinSeg, (share + kChunk - 1) / kChunk * kChunk);
+    return static_cast<int>(std::min<int64_t>(len, 0x40000000));
+}
+
+struct LinLayout {
+    int seg_len, max_items, max_bounds;
+    size_t items, multi, z, zdecay, total;
+};
+LinLayout layout(int64_t total_tokens, int n_seqs, int H, int dk, int dv) {
+    LinLayout l{};
+    l.seg_len = segment_tokens(total_tokens, H);
+    l.max_bounds = static_cast<int>(total_tokens / l.seg_len);   // every segment with a successor is full
+    l.max_items = n_seqs + l.max_bounds;
+    size_t at = round256(sizeof(LinHead));
+    auto take = [&](size_t bytes) {
+        const size_t p = at;
+        at += round256(bytes);
+        return p;
+    };
+    l.items = take(sizeof(LinItem) * static_cast<size_t>(l.max_items));
+    l.multi = take(sizeof(int2) * static_cast<size_t>(l.max_bounds));
+    l.z = take(sizeof(float) * static_cast<size_t>(l.max_bounds) * H * dk * dv);
+    l.zdecay = take(sizeof(float) * static_cast<size_t>(l.max_bounds) * H);
+    l.total = at;
+    return l;
+}
+
+}  // namespace
+
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" {
+
+size_t kda_lin_chunk_fwd_workspace_bytes(int64_t total_tokens, int n_seqs, int H, int dk, int dv, kda_dtype_t dtype) {
+    if (total_tokens < 0 || total_tokens > 0x7fffffffLL || n_seqs < 0 || H <= 0 || !dims_ok(dk, dv)) return 0;
+    if (dtype != KDA_BF16 && dtype != KDA_F32) return 0;
+    if (n_seqs > 0x3fffffff) return 0;
+    return layout(total_tokens, n_seqs, H, dk, dv).total;
+}
+
+kda_status_t kda_lin_chunk_fwd(const void* q, const void* k, const void* v, const float* log_alpha, int la_per_token,
+                               const float* initial_state, const int32_t* cu_seqlens, int n_seqs,
+                               int64_t total_tokens, int Hqk, int H, int dk, int dv, kda_dtype_t dtype,
+                               int ckpt_stride, void* o, float* final_state, float* checkpoints,
+                               const int32_t* ckpt_cu, void* workspace, size_t ws_bytes, kda_stream_t stream) {
+    if (n_seqs < 0 || n_seqs > 0x3fffffff || total_tokens < 0 || H <= 0 || Hqk <= 0 || H % Hqk != 0 || ckpt_stride < 0 ||
+        (la_per_token != 0 && la_per_token != 1))
+        return KDA_ERR_ARG;
+    if (total_tokens > 0x7fffffffLL) return KDA_ERR_ARG;   // cu_seqlens is int32
+    if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_ARG;
+    if (!dims_ok(dk, dv)) return KDA_ERR_UNSUPPORTED;
+    if (ckpt_stride > 0 && (ckpt_stride % kChunk != 0 || !checkpoints || !ckpt_cu)) return KDA_ERR_ARG;
+    if (n_seqs == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_ARG;
+    if (!cu_seqlens || !workspace) return KDA_ERR_ARG;
+    if (total_tokens > 0 && (!q || !k || !v || !log_alpha || !o)) return KDA_ERR_ARG;
+    const void* ptrs[] = {q, k, v, initial_state, o, final_state, checkpoints};
+    for (const void* p : ptrs)
+        if (p && !aligned(p, 16)) return KDA_ERR_ALIGN;
+    if ((log_alpha && !aligned(log_alpha, 4)) || !aligned(cu_seqlens, 4) || (ckpt_cu && !aligned(ckpt_cu, 4)))
+        return KDA_ERR_ALIGN;
+    if (!aligned(workspace, 256)) return KDA_ERR_ALIGN;
+    const LinLayout l = layout(total_tokens, n_seqs, H, dk, dv);
+    if (ws_bytes < l.total) return KDA_ERR_WORKSPACE;
+    if (static_cast<long long>(l.max_items) * H > 0x7fffffffLL) return KDA_ERR_ARG;
+
+    char* ws = static_cast<char*>(workspace);
+    LinArgs a{};
+    a.q = q; a.k = k; a.v = v; a.la = log_alpha; a.la_t = la_per_token ? H : 0; a.la_h = 1;
+    a.initial_state = initial_state; a.cu_seqlens = cu_seqlens; a.n_seqs = n_seqs; a.total_tokens = total_tokens;
+    a.Hqk = Hqk; a.H = H; a.dk = dk; a.dv = dv; a.ckpt_stride = ckpt_stride; a.o = o; a.final_state = final_state;
+    a.checkpoints = checkpoints; a.ckpt_cu = ckpt_cu;
+    a.head = reinterpret_cast<LinHead*>(ws);
+    a.items = reinterpret_cast<LinItem*>(ws + l.items);
+    a.multi = reinterpret_cast<int2*>(ws + l.multi);
+    a.z = reinterpret_cast<float*>(ws + l.z);
+    a.zdecay = reinterpret_cast<float*>(ws + l.zdecay);
+    a.max_items = l.max_items; a.max_bounds = l.max_bounds; a.seg_len = l.seg_len;
+    a.status = status_ptr();
+    if (!a.status) return KDA_ERR_CUDA;
+
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool bf16 = dtype == KDA_BF16;
+    if (launch_chained(lin_index_kernel, dim3(1), dim3(1024), s, cu_seqlens, n_seqs, static_cast<int>(total_tokens),
+                       l.seg_len, l.max_items, a.head, a.items, a.multi, a.status) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    if (l.max_bounds > 0) {
+        if (launch_lin_simt(a, bf16, true, s) != cudaSuccess) return KDA_ERR_CUDA;
+        const int elems = dk * dv;
+        const unsigned bx = static_cast<unsigned>((static_cast<size_t>(H) * elems / 4 + 255) / 256);
+        const dim3 grid(bx, static_cast<unsigned>(std::min(l.max_bounds, 64)));
+        if (launch_chained(lin_join_kernel, grid, dim3(256), s, a.head, a.multi, a.z, a.zdecay, H, elems) != cudaSuccess)
+            return KDA_ERR_CUDA;
+    }
+    return launch_lin_simt(a, bf16, false, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status_t kda_lin_recurrent_step(float* state, int64_t n_states, const int32_t* slots, int slot_stride,
+                                    const void* q, const void* k, const void* v, const float* log_alpha,
+                                    int la_per_token, int n, int Hqk, int H, int dk, int dv, kda_dtype_t dtype,
+                                    void* o, kda_stream_t stream) {
+    if (n < 0 || H <= 0 || Hqk <= 0 || H % Hqk != 0 || n_states < 0 || (la_per_token != 0 && la_per_token != 1))
+        return KDA_ERR_ARG;
+    if (slots ? slot_stride <= 0 : n > n_states) return KDA_ERR_ARG;
+    if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_ARG;
+    if (!dims_ok(dk, dv)) return KDA_ERR_UNSUPPORTED;
+    if (n == 0) return KDA_OK;
+    if (!q || !k || !v || !log_alpha || !o || (!state && n_states > 0)) return KDA_ERR_ARG;
+    const size_t es = dtype == KDA_BF16 ? 2 : 4;
+    if (!aligned(state, 16) || !aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(o, es) ||
+        !aligned(log_alpha, 4) || (slots && !aligned(slots, 4)))
+        return KDA_ERR_ALIGN;
+    if (static_cast<long long>(n) * H * (dv / 32) > 0x7fffffffLL) return KDA_ERR_ARG;
+    int* st = status_ptr();
+    if (!st) return KDA_ERR_CUDA;
+    return launch_lin_step(state, n_states, slots, slot_stride, q, k, v, log_alpha, la_per_token, n, Hqk, H, dk, dv,
+                           dtype == KDA_BF16, o, st, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

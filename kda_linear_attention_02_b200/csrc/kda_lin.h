@@ -1,0 +1,71 @@
+// kda_lin.h -- what the translation units of the decayed linear attention share (kda_lin_*.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_internal.h"
+
+namespace kda {
+
+// A decay below e^-120 is 0 in fp32, and so is every product with it: clamping the logarithm there leaves
+// alpha as it is and keeps sums of logarithms finite (minus infinity and NaN become -120 too).
+constexpr float kLinLogMin = -120.f;
+
+// One segment of a sequence: what one CTA (of each head and slice) walks through, chunk by chunk.
+struct __align__(16) LinItem {
+    int seq;     // sequence
+    int seg;     // segment within the sequence
+    int n_seg;   // segments of the sequence
+    int t0;      // first token, in the packed batch
+    int n;       // tokens
+    int pos;     // tokens of the sequence ahead of the segment (a multiple of kChunk)
+    int z0;      // first boundary of the sequence: boundary z0 + s lies between its segments s and s + 1
+    int pad;
+};
+
+// Workspace header, followed by the items, the sequences with more than one segment, and per boundary and
+// head a state [dk, dv] and the decay of the segment ahead of it.
+struct __align__(16) LinHead {
+    int n_items;
+    int n_multi;
+    int pad[2];
+};
+
+struct LinArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* la;
+    int la_t, la_h;              // log_alpha of (token, head) is la[token * la_t + head * la_h]
+    const float* initial_state;
+    const int32_t* cu_seqlens;
+    int n_seqs;
+    int64_t total_tokens;
+    int Hqk, H, dk, dv;
+    int ckpt_stride;
+    void* o;
+    float* final_state;
+    float* checkpoints;
+    const int32_t* ckpt_cu;
+    // workspace parts
+    LinHead* head;
+    LinItem* items;
+    int2* multi;                 // {first item's sequence boundary z0, segments} of the sequences with several
+    float* z;                    // [boundaries, H, dk, dv]
+    float* zdecay;               // [boundaries, H]
+    int max_items, max_bounds;   // bounds the host knows
+    int seg_len;                 // tokens per segment (a multiple of kChunk)
+    int* status;
+};
+
+// One pass over all segments (kda_lin_simt.cu: both types; kda_lin_bf16.cu: bf16 on the tensor cores).
+// boundary_pass: only the segments with a successor, only their end states, into z and zdecay.
+cudaError_t launch_lin_simt(const LinArgs& a, bool bf16, bool boundary_pass, cudaStream_t s);
+
+// Decode step (kda_lin_step.cu).
+cudaError_t launch_lin_step(float* state, int64_t n_states, const int32_t* slots, int slot_stride, const void* q,
+                            const void* k, const void* v, const float* la, int la_per_token, int n, int Hqk, int H,
+                            int dk, int dv, bool bf16, void* o, int* status, cudaStream_t s);
+
+}  // namespace kda
