@@ -229,14 +229,14 @@ kda_status_t kda_lin_chunk_fwd(const void* q, const void* k, const void* v, cons
                        l.seg_len, l.max_items, a.head, a.items, a.multi, a.status) != cudaSuccess)
         return KDA_ERR_CUDA;
     if (l.max_bounds > 0) {
-        if (launch_lin_simt(a, bf16, true, s) != cudaSuccess) return KDA_ERR_CUDA;
+        if ((bf16 ? launch_lin_bf16(a, true, s) : launch_lin_simt(a, true, s)) != cudaSuccess) return KDA_ERR_CUDA;
         const int elems = dk * dv;
         const unsigned bx = static_cast<unsigned>((static_cast<size_t>(H) * elems / 4 + 255) / 256);
         const dim3 grid(bx, static_cast<unsigned>(std::min(l.max_bounds, 64)));
         if (launch_chained(lin_join_kernel, grid, dim3(256), s, a.head, a.multi, a.z, a.zdecay, H, elems) != cudaSuccess)
             return KDA_ERR_CUDA;
     }
-    return launch_lin_simt(a, bf16, false, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return (bf16 ? launch_lin_bf16(a, false, s) : launch_lin_simt(a, false, s)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 kda_status_t kda_lin_recurrent_step(float* state, int64_t n_states, const int32_t* slots, int slot_stride,

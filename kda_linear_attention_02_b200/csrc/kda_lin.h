@@ -59,9 +59,10 @@ struct LinArgs {
     int* status;
 };
 
-// One pass over all segments (kda_lin_simt.cu: both types; kda_lin_bf16.cu: bf16 on the tensor cores).
+// One pass over all segments (kda_lin_simt.cu: fp32 on the fp32 units; kda_lin_bf16.cu: bf16 on the tensor cores).
 // boundary_pass: only the segments with a successor, only their end states, into z and zdecay.
-cudaError_t launch_lin_simt(const LinArgs& a, bool bf16, bool boundary_pass, cudaStream_t s);
+cudaError_t launch_lin_simt(const LinArgs& a, bool boundary_pass, cudaStream_t s);
+cudaError_t launch_lin_bf16(const LinArgs& a, bool boundary_pass, cudaStream_t s);
 
 // Decode step (kda_lin_step.cu).
 cudaError_t launch_lin_step(float* state, int64_t n_states, const int32_t* slots, int slot_stride, const void* q,

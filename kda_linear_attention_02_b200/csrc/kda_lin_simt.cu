@@ -1,4 +1,4 @@
-// kda_lin_simt.cu -- decayed linear attention, chunked form, on the fp32 units.
+// kda_lin_simt.cu -- decayed linear attention, chunked form, fp32 on the fp32 units.
 //
 // A CTA walks one segment of one (sequence, head) in chunks of C = 32 tokens and holds 32 of the state's dv
 // columns.  With g_t = sum of log_alpha over tokens 1..t of the chunk,
@@ -25,37 +25,18 @@ struct SimtSmem {
     float eg[kC], w[kC];
 };
 
-// 16 bytes of row elements as floats
-__device__ __forceinline__ void load16(const float* p, float* x) {
-    const float4 f = *reinterpret_cast<const float4*>(p);
-    x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
-}
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float* x) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t r[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(r[i] << 16);
-        x[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
-    }
-}
-
 // rows 0..n-1 of a [C, COLS] tile (row pitch in elements), zeros behind them
-template <typename T, int COLS, int PITCH>
-__device__ __forceinline__ void load_tile(float (*dst)[PITCH], const T* src, size_t pitch, int n) {
-    constexpr int E = 16 / sizeof(T), V = COLS / E;
+template <int COLS, int PITCH>
+__device__ __forceinline__ void load_tile(float (*dst)[PITCH], const float* src, size_t pitch, int n) {
+    constexpr int V = COLS / 4;
     for (int i = threadIdx.x; i < kC * V; i += kNt) {
-        const int r = i / V, c = i % V * E;
-        float x[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = 0.f;
-        if (r < n) load16(src + r * pitch + c, x);
-#pragma unroll
-        for (int e = 0; e < E; ++e) dst[r][c + e] = x[e];
+        const int r = i / V, c = i % V * 4;
+        *reinterpret_cast<float4*>(&dst[r][c]) =
+            r < n ? *reinterpret_cast<const float4*>(src + r * pitch + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
-template <typename T, int DK, bool BOUNDARY>
+template <int DK, bool BOUNDARY>
 __global__ void __launch_bounds__(kNt) lin_simt_kernel(const LinArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     SimtSmem<DK>& sh = *reinterpret_cast<SimtSmem<DK>*>(smem_raw);
@@ -87,18 +68,18 @@ __global__ void __launch_bounds__(kNt) lin_simt_kernel(const LinArgs a) {
         for (int r = 0; r < R; ++r) *reinterpret_cast<float4*>(dst + (r0 + r) * dv + j0 + c0) = S[r];
     };
 
-    const T* Q = static_cast<const T*>(a.q);
-    const T* K = static_cast<const T*>(a.k);
-    const T* V = static_cast<const T*>(a.v);
-    T* O = static_cast<T*>(a.o);
+    const float* Q = static_cast<const float*>(a.q);
+    const float* K = static_cast<const float*>(a.k);
+    const float* V = static_cast<const float*>(a.v);
+    float* O = static_cast<float*>(a.o);
     const size_t pq = static_cast<size_t>(a.Hqk) * DK, pv = static_cast<size_t>(a.H) * dv;
     double total = 0.0;   // sum of log_alpha over the segment (warp 0)
     for (int c = 0; c < it.n; c += kC) {
         const size_t tok = static_cast<size_t>(it.t0) + c;
         const int n = min(kC, it.n - c);
-        if (!BOUNDARY) load_tile<T, DK>(sh.q, Q + tok * pq + static_cast<size_t>(hq) * DK, pq, n);
-        load_tile<T, DK>(sh.k, K + tok * pq + static_cast<size_t>(hq) * DK, pq, n);
-        load_tile<T, kDvs>(sh.v, V + tok * pv + static_cast<size_t>(h) * dv + j0, pv, n);
+        if (!BOUNDARY) load_tile<DK>(sh.q, Q + tok * pq + static_cast<size_t>(hq) * DK, pq, n);
+        load_tile<DK>(sh.k, K + tok * pq + static_cast<size_t>(hq) * DK, pq, n);
+        load_tile<kDvs>(sh.v, V + tok * pv + static_cast<size_t>(h) * dv + j0, pv, n);
         if (w == 0) {
             const double x = lane < n ? static_cast<double>(fmaxf(a.la[(tok + lane) * a.la_t + static_cast<size_t>(h) * a.la_h], kLinLogMin)) : 0.0;
             double g = x, r = x;   // inclusive sums from the start and from the end
@@ -152,13 +133,8 @@ __global__ void __launch_bounds__(kNt) lin_simt_kernel(const LinArgs a) {
                     x = make_float4(fmaf(p, vv.x, x.x), fmaf(p, vv.y, x.y), fmaf(p, vv.z, x.z), fmaf(p, vv.w, x.w));
                 }
                 const float e = sh.eg[row];
-                const float ov[4] = {fmaf(e, y.x, x.x), fmaf(e, y.y, x.y), fmaf(e, y.z, x.z), fmaf(e, y.w, x.w)};
-                T* dst = O + (tok + row) * pv + static_cast<size_t>(h) * dv + j0 + c0;
-                if constexpr (sizeof(T) == 4) {
-                    *reinterpret_cast<float4*>(dst) = make_float4(ov[0], ov[1], ov[2], ov[3]);
-                } else {
-                    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(ov[0], ov[1]), pack_bf16x2(ov[2], ov[3]));
-                }
+                *reinterpret_cast<float4*>(O + (tok + row) * pv + static_cast<size_t>(h) * dv + j0 + c0) =
+                    make_float4(fmaf(e, y.x, x.x), fmaf(e, y.y, x.y), fmaf(e, y.z, x.z), fmaf(e, y.w, x.w));
             }
         }
         // rows behind the sequence's end have log_alpha 0 and k, v of zeros
@@ -197,10 +173,10 @@ __global__ void __launch_bounds__(kNt) lin_simt_kernel(const LinArgs a) {
     }
 }
 
-template <typename T, int DK, bool BOUNDARY>
+template <int DK, bool BOUNDARY>
 cudaError_t launch(const LinArgs& a, cudaStream_t s) {
     constexpr int smem = sizeof(SimtSmem<DK>);
-    cudaError_t e = cudaFuncSetAttribute(lin_simt_kernel<T, DK, BOUNDARY>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(lin_simt_kernel<DK, BOUNDARY>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.max_items * a.H), a.dv / kDvs);
@@ -212,18 +188,14 @@ cudaError_t launch(const LinArgs& a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lin_simt_kernel<T, DK, BOUNDARY>, a);
+    return cudaLaunchKernelEx(&cfg, lin_simt_kernel<DK, BOUNDARY>, a);
 }
 
 }  // namespace
 
-cudaError_t launch_lin_simt(const LinArgs& a, bool bf16, bool boundary_pass, cudaStream_t s) {
-    if (bf16) {
-        if (a.dk == 64) return boundary_pass ? launch<__nv_bfloat16, 64, true>(a, s) : launch<__nv_bfloat16, 64, false>(a, s);
-        return boundary_pass ? launch<__nv_bfloat16, 128, true>(a, s) : launch<__nv_bfloat16, 128, false>(a, s);
-    }
-    if (a.dk == 64) return boundary_pass ? launch<float, 64, true>(a, s) : launch<float, 64, false>(a, s);
-    return boundary_pass ? launch<float, 128, true>(a, s) : launch<float, 128, false>(a, s);
+cudaError_t launch_lin_simt(const LinArgs& a, bool boundary_pass, cudaStream_t s) {
+    if (a.dk == 64) return boundary_pass ? launch<64, true>(a, s) : launch<64, false>(a, s);
+    return boundary_pass ? launch<128, true>(a, s) : launch<128, false>(a, s);
 }
 
 }  // namespace kda
