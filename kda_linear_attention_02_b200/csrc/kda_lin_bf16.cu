@@ -66,6 +66,20 @@ struct Decays {            // of one chunk
 __device__ __forceinline__ float lo_f32(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
+// One lane of a converged warp, always the same one.  The MMAs are issued under this predicate by a warp whose
+// addresses are warp-uniform values: issued by a lane chosen with threadIdx, from values the compiler cannot
+// see to be uniform, each costs about 96 cycles; so, 32 to 64 (M = 128, K = 16, N = 64 to 128).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
     tmem_st16(taddr, reinterpret_cast<const float(&)[16]>(v));
 }
@@ -82,7 +96,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
     __shared__ __align__(8) uint64_t full[NST], empty[NST], sp_full, sp_free, p_ready[2], p_free[2], w_ready, z_full,
         z_free, sb_ready, sb_free, o_full, o_free, done;
     __shared__ uint32_t tmem_slot;
-    const int t = threadIdx.x, w = t >> 5, lane = t & 31;
+    const int t = threadIdx.x, w = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
     if (t == 0) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(&full[s], 2);
@@ -177,67 +191,80 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         for (int c = issued > NST ? issued - NST : 0; c < issued; ++c) mbar_wait(&full[c % NST], (c / NST) & 1, nullptr);
     } else if (w == 3) {
         // ---------------- issuer
-        if (lane == 0) {
-            constexpr uint32_t id_sp = idesc_bf16(128, C), id_o1 = idesc_bf16(128, C),
-                               id_o2 = idesc_bf16(128, C, false, false, true), id_z = idesc_bf16(128, DK, false, true);
-            auto scores = [&](int c) {
-                const uint32_t q = smem_u32(sm + (c % NST) * F::STAGE), k = q + F::QB;
+        constexpr uint32_t id_sp = idesc_bf16(128, C), id_o1 = idesc_bf16(128, C),
+                           id_o2 = idesc_bf16(128, C, false, false, true), id_z = idesc_bf16(128, DK, false, true);
+        const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0), base = __shfl_sync(0xffffffffu, smem_u32(sm), 0);
+        auto scores = [&](int s) {
+            const uint32_t q = base + s * F::STAGE, k = q + F::QB;
+            const uint64_t qd = sdesc_k_sw128(q), kd = sdesc_k_sw128(k);
+            if (elect_one()) {
 #pragma unroll
                 for (int i = 0; i < DK / 16; ++i) {
-                    const uint32_t off = (i / 4) * F::HALF + (i % 4) * 32;
-                    umma_f16(tm + F::SP, sdesc_k_sw128(q + off), sdesc_k_sw128(k + off), id_sp, i > 0);
+                    const uint32_t off = ((i / 4) * F::HALF + (i % 4) * 32) >> 4;
+                    umma_f16(tmu + F::SP, qd + off, kd + off, id_sp, i > 0);
                 }
                 umma_commit(&sp_full);
-            };
-            bool ok = true;
-            if (!BOUNDARY && nch > 0) {
-                ok = mbar_wait(&full[0], 0, status);
-                if (ok) scores(0);
             }
-            for (int c = 0; ok && c < nch; ++c) {
-                const int s = c % NST;
-                const uint32_t q = smem_u32(sm + s * F::STAGE), k = q + F::QB, v = k + F::KB;
-                if (!mbar_wait(&full[s], (c / NST) & 1, status)) break;
-                if (!mbar_wait(&w_ready, c & 1, status)) break;
-                if (c > 0 && !mbar_wait(&z_free, (c - 1) & 1, status)) break;
-                tc_fence_after();
+            __syncwarp();
+        };
+        if (!BOUNDARY && nch > 0 && mbar_wait(&full[0], 0, status)) scores(0);
+        int s = 0, ph = 0;   // stage of chunk c, and the parity of its use
+        for (int c = 0; c < nch; ++c) {
+            const uint32_t q = base + s * F::STAGE, k = q + F::QB, v = k + F::KB;
+            const int s1 = s + 1 == NST ? 0 : s + 1, ph1 = s + 1 == NST ? ph ^ 1 : ph;
+            if (!mbar_wait(&full[s], ph, status)) break;
+            if (!mbar_wait(&w_ready, c & 1, status)) break;
+            if (c > 0 && !mbar_wait(&z_free, (c - 1) & 1, status)) break;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t kd = sdesc_mn_sw128(k, F::HALF);
 #pragma unroll
                 for (int p = 0; p < 3; ++p)
 #pragma unroll
                     for (int i = 0; i < C / 16; ++i)
-                        umma_f16_ts(tm + F::Z, tm + F::W + 32 * p + 8 * i, sdesc_mn_sw128(k + i * 2048, F::HALF), id_z,
-                                    p > 0 || i > 0);
+                        umma_f16_ts(tmu + F::Z, tmu + F::W + 32 * p + 8 * i, kd + i * (2048 >> 4), id_z, p > 0 || i > 0);
                 umma_commit(&z_full);
-                if (!BOUNDARY) {
-                    if (c + 1 < nch) {
-                        if (!mbar_wait(&full[(c + 1) % NST], ((c + 1) / NST) & 1, status)) break;
-                        if (!mbar_wait(&sp_free, c & 1, status)) break;
-                        tc_fence_after();
-                        scores(c + 1);
-                    }
-                    if (!mbar_wait(&sb_ready, c & 1, status)) break;
-                    if (c > 0 && !mbar_wait(&o_free, (c - 1) & 1, status)) break;
+            }
+            __syncwarp();
+            if (!BOUNDARY) {
+                if (c + 1 < nch) {
+                    if (!mbar_wait(&full[s1], ph1, status)) break;
+                    if (!mbar_wait(&sp_free, c & 1, status)) break;
                     tc_fence_after();
+                    scores(s1);
+                }
+                if (!mbar_wait(&sb_ready, c & 1, status)) break;
+                if (c > 0 && !mbar_wait(&o_free, (c - 1) & 1, status)) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t qd = sdesc_k_sw128(q);
 #pragma unroll
                     for (int i = 0; i < DK / 16; ++i)
-                        umma_f16_ts(tm + F::O1, tm + F::SB + 8 * i, sdesc_k_sw128(q + (i / 4) * F::HALF + (i % 4) * 32), id_o1,
+                        umma_f16_ts(tmu + F::O1, tmu + F::SB + 8 * i, qd + (((i / 4) * F::HALF + (i % 4) * 32) >> 4), id_o1,
                                     i > 0);
                     umma_commit(&sb_free);
-                    if (!mbar_wait(&p_ready[c & 1], (c >> 1) & 1, status)) break;
-                    tc_fence_after();
-                    const uint32_t p = smem_u32(sm + F::P0 + (c & 1) * F::PB);
+                }
+                __syncwarp();
+                if (!mbar_wait(&p_ready[c & 1], (c >> 1) & 1, status)) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t vd = sdesc_mn_sw128(v, F::HALF), pd = sdesc_k_sw128(base + F::P0 + (c & 1) * F::PB);
 #pragma unroll
                     for (int i = 0; i < C / 16; ++i)
-                        umma_f16(tm + F::O2, sdesc_mn_sw128(v + i * 2048, F::HALF), sdesc_k_sw128(p + i * 32), id_o2, i > 0);
+                        umma_f16(tmu + F::O2, vd + i * (2048 >> 4), pd + i * (32 >> 4), id_o2, i > 0);
                     umma_commit(&o_full);
                     umma_commit(&p_free[c & 1]);
                 }
-                umma_commit(&empty[s]);
+                __syncwarp();
             }
-            umma_commit(&done);
-            mbar_wait(&done, 0, nullptr);   // no product stays in flight behind the CTA
+            if (elect_one()) umma_commit(&empty[s]);
+            __syncwarp();
+            s = s1;
+            ph = ph1;
         }
+        if (elect_one()) umma_commit(&done);
         __syncwarp();
+        mbar_wait(&done, 0, nullptr);   // no product stays in flight behind the CTA
     } else if (w < 2) {
         // ---------------- P: warp w has rows 32 w .. 32 w + 31; columns above the diagonal blocks stay zero
         if (!BOUNDARY) {
@@ -254,38 +281,34 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 tc_fence_after();
                 const Decays& d = decays[s];
                 const float gr = d.g2[row];
-                uint32_t pk[32];
-                auto block = [&](int j0, uint32_t* out) {   // columns j0 .. j0 + 31
-                    float x[32];
-                    const uint32_t at = tm + F::SP + (static_cast<uint32_t>(32 * w) << 16) + j0;
-                    tmem_ld16(at, *reinterpret_cast<float(*)[16]>(x));
-                    tmem_ld16(at + 16, *reinterpret_cast<float(*)[16]>(x + 16));
-                    tmem_wait_ld_regs<32>(x);
+                if (c >= 2 && !mbar_wait(&p_free[c & 1], ((c >> 1) - 1) & 1, status)) break;
+                uint8_t* p = p0 + (c & 1) * F::PB;
+#pragma unroll 1
+                for (int j0 = 0; j0 < 32 * (w + 1); j0 += 16) {
+                    float x[16];
+                    tmem_ld16(tm + F::SP + (static_cast<uint32_t>(32 * w) << 16) + j0, x);
+                    tmem_wait_ld_regs<16>(x);
+                    uint32_t u[8];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
+                    for (int j = 0; j < 16; j += 4) {
                         const float4 g = *reinterpret_cast<const float4*>(&d.g2[j0 + j]);
-                        const float e0 = ex2_approx(gr - g.x), e1 = ex2_approx(gr - g.y), e2 = ex2_approx(gr - g.z),
-                                    e3 = ex2_approx(gr - g.w);
-                        out[j / 2] = pack_bf16x2(j0 + j <= row ? x[j] * e0 : 0.f, j0 + j + 1 <= row ? x[j + 1] * e1 : 0.f);
-                        out[j / 2 + 1] =
-                            pack_bf16x2(j0 + j + 2 <= row ? x[j + 2] * e2 : 0.f, j0 + j + 3 <= row ? x[j + 3] * e3 : 0.f);
+                        const int k = row - j0 - j;   // columns up to k are on or under the diagonal
+                        u[j / 2] = pack_bf16x2(k >= 0 ? x[j] * ex2_approx(gr - g.x) : 0.f,
+                                               k >= 1 ? x[j + 1] * ex2_approx(gr - g.y) : 0.f);
+                        u[j / 2 + 1] = pack_bf16x2(k >= 2 ? x[j + 2] * ex2_approx(gr - g.z) : 0.f,
+                                                   k >= 3 ? x[j + 3] * ex2_approx(gr - g.w) : 0.f);
                     }
-                };
-                block(0, pk);
-                if (w == 1) block(32, pk + 16);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        *reinterpret_cast<uint4*>(p + (((j0 / 8 + i) ^ (row & 7)) << 4)) =
+                            make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&sp_free);
                     mbar_arrive(&empty[s]);
                 }
-                if (c >= 2 && !mbar_wait(&p_free[c & 1], ((c >> 1) - 1) & 1, status)) break;
-                uint8_t* p = p0 + (c & 1) * F::PB;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < 4 || w == 1)
-                        *reinterpret_cast<uint4*>(p + ((i ^ (row & 7)) << 4)) =
-                            make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_ready[c & 1]);
@@ -324,34 +347,31 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             if (mine && ok) {
                 tc_fence_after();
                 const Decays& d = decays[s];
+#pragma unroll 1
+                for (int b = 0; b < C; b += 16) {   // 16 tokens: 8 packed columns of each part
+                    uint32_t u[3][8];
 #pragma unroll
-                for (int b = 0; b < C; b += 32) {
-                    uint32_t hi[16], mid[16], lo[16];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
+                    for (int j = 0; j < 16; j += 4) {
                         const float4 wt = *reinterpret_cast<const float4*>(&d.w[b + j]);
                         const float wv[4] = {wt.x, wt.y, wt.z, wt.w};
 #pragma unroll
                         for (int e = 0; e < 4; e += 2) {
-                            const int r = b + j + e;
-                            const uint8_t* p = vt + (r >> 3) * 1024;
+                            const int r = j + e;   // its eight-row group starts at token b + (r & 8)
+                            const uint8_t* p = vt + (b + (r & 8)) * 128;
                             const uint32_t v0 = *reinterpret_cast<const unsigned short*>(p + off[r & 7]);
                             const uint32_t v1 = *reinterpret_cast<const unsigned short*>(p + off[(r + 1) & 7]);
                             float f0 = wv[e] * lo_f32(v0), f1 = wv[e + 1] * lo_f32(v1);
-                            const uint32_t u = pack_bf16x2(f0, f1);
-                            f0 -= lo_f32(u);
-                            f1 -= hi_f32(u);
-                            const uint32_t m = pack_bf16x2(f0, f1);
-                            f0 -= lo_f32(m);
-                            f1 -= hi_f32(m);
-                            hi[(j + e) / 2] = u;
-                            mid[(j + e) / 2] = m;
-                            lo[(j + e) / 2] = pack_bf16x2(f0, f1);
+#pragma unroll
+                            for (int k = 0; k < 3; ++k) {
+                                const uint32_t x = pack_bf16x2(f0, f1);
+                                u[k][r / 2] = x;
+                                f0 -= lo_f32(x);
+                                f1 -= hi_f32(x);
+                            }
                         }
                     }
-                    tmem_st16u(tm + lanes + F::W + b / 2, hi);
-                    tmem_st16u(tm + lanes + F::W + 32 + b / 2, mid);
-                    tmem_st16u(tm + lanes + F::W + 64 + b / 2, lo);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) tmem_st8(tm + lanes + F::W + 32 * k + b / 2, u[k]);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -372,7 +392,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             if (mine && ok) {
                 tc_fence_after();
                 const Decays& d = decays[s];
-#pragma unroll
+#pragma unroll 1
                 for (int b = 0; b < C; b += 16) {
                     float x[16], y[16];
                     tmem_ld16(tm + lanes + F::O1 + b, x);
@@ -386,7 +406,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         const float ev[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            *reinterpret_cast<__nv_bfloat16*>(ob + ((b + j + i) >> 3) * 1024 + off[(b + j + i) & 7]) =
+                            *reinterpret_cast<__nv_bfloat16*>(ob + (b + ((j + i) & 8)) * 128 + off[(j + i) & 7]) =
                                 __float2bfloat16_rn(fmaf(ev[i], x[j + i], y[j + i]));
                     }
                 }
