@@ -28,6 +28,7 @@ __global__ void __launch_bounds__(1024) lin_index_kernel(const int32_t* __restri
     __shared__ long long warp_sums[32];
     __shared__ int lens[1024];
     __shared__ int s_multi;
+    grid_launch_dependents();
     grid_dependency_wait();
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     if (t == 0) s_multi = 0;
@@ -99,6 +100,7 @@ __global__ void __launch_bounds__(1024) lin_index_kernel(const int32_t* __restri
 __global__ void __launch_bounds__(256) lin_join_kernel(const LinHead* __restrict__ head, const int2* __restrict__ multi,
                                                        float* __restrict__ z, const float* __restrict__ zdecay, int H,
                                                        int elems) {
+    grid_launch_dependents();
     grid_dependency_wait();
     const int e4 = (blockIdx.x * 256 + threadIdx.x) * 4, h = e4 / elems;
     if (h >= H) return;

@@ -12,6 +12,10 @@ namespace kda {
 // alpha as it is and keeps sums of logarithms finite (minus infinity and NaN become -120 too).
 constexpr float kLinLogMin = -120.f;
 
+// Lets the next kernel of the stream, launched with programmatic serialization, take its place on the SMs once
+// every block of this one has started; it still waits for this one's end before it touches memory.
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // One segment of a sequence: what one CTA (of each head and slice) walks through, chunk by chunk.
 struct __align__(16) LinItem {
     int seq;     // sequence

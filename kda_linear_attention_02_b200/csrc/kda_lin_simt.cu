@@ -40,6 +40,7 @@ template <int DK, bool BOUNDARY>
 __global__ void __launch_bounds__(kNt) lin_simt_kernel(const LinArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     SimtSmem<DK>& sh = *reinterpret_cast<SimtSmem<DK>*>(smem_raw);
+    grid_launch_dependents();
     grid_dependency_wait();
     const int item = blockIdx.x / a.H, h = blockIdx.x % a.H, j0 = blockIdx.y * kDvs;
     if (item >= a.head->n_items) return;

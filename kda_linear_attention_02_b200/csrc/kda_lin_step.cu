@@ -22,6 +22,7 @@ __global__ void __launch_bounds__(NT) lin_step_kernel(float* __restrict__ state,
     __shared__ float4 red[RG][CG];
     const int t = threadIdx.x, cg = t % CG, rg = t / CG;
     const int i = blockIdx.x / H, h = blockIdx.x % H, j0 = blockIdx.y * DVS, hq = h / (H / Hqk);
+    grid_launch_dependents();
     grid_dependency_wait();
     long long slot = i;
     if (slots) {
