@@ -13,8 +13,8 @@
 // too.  What reaches o is rounded once in each path (P, and the copy of S).  What reaches the state is not: k
 // and v are bf16 already, and W goes in as four bf16 parts that add up to w v to 24 bits, so Z is an fp32 sum
 // of exact products.  With w = w1 + w2 + w3 in bf16 parts, packed bf16 FMAs give them two tokens at a time,
-//     h = rn(w1 v),  e = w1 v - h (exact: eight bits are left),  m = rn(w2 v),  l = rn(w3 v + (w2 v - m)),
-// five instructions a pair; splitting the fp32 products w v takes seventeen and was what bounded the kernel.  Z starts from zero in every chunk and joins S by one rounded FMA: an
+//     h = rn(w1 v),  -e = h - w1 v (exact: eight bits are left),  m = rn(w2 v),  -l = rn((m - w2 v) - w3 v),
+// five instructions a pair (splitting the fp32 products w v takes seventeen); the MMAs negate -e and -l.  Z starts from zero in every chunk and joins S by one rounded FMA: an
 // accumulator that lived on in tensor memory would collect the truncation of its additions over the length of
 // the sequence.
 //
@@ -49,6 +49,7 @@ struct Cfg {
     static constexpr uint32_t P0 = NST * STAGE, O0 = P0 + (BOUNDARY ? 0 : 2 * PB);
     // the A operands of 128 rows read past 64-row tiles (their results are not used): the tiles behind exist
     static constexpr uint32_t BYTES = O0 + (BOUNDARY ? HALF : 2 * VB);
+    static constexpr int ZN = DK;   // channels of k that one piece of Z has
     // tensor memory columns
     static constexpr uint32_t SP = 0, O1 = 64, O2 = 128, Z = 192, SB = 320, W = 384, COLS = 512;   // W: 4 x 32
     static_assert(BYTES + 1024 + 4096 <= 227 * 1024, "shared memory");
@@ -62,7 +63,7 @@ constexpr int kRegsState = 176, kRegsOther = 112;
 struct Decays {            // of one chunk
     float g2[kChunk];      // g_t log2(e)
     float eg[kChunk];      // e^{g_t}
-    uint4 w[kChunk / 2];   // of tokens 2 i, 2 i + 1: the three bf16 parts of e^{g_C - g_t}, packed pairs
+    uint4 w[kChunk / 2];   // of tokens 2 i, 2 i + 1: the bf16 parts w1, w2, -w3 of e^{g_C - g_t}, packed pairs
     float m[kChunk / 2];   // e^{g_32 - g_t} of the chunk's first half
     float g2m;             // g_32 log2(e)
     float eC;              // e^{g_C}
@@ -104,12 +105,6 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
-__device__ __forceinline__ uint32_t neg_bf16x2(uint32_t a) {
-    uint32_t d;
-    asm("neg.bf16x2 %0, %1;" : "=r"(d) : "r"(a));
-    return d;
-}
-
 // 16 lanes x 32 columns of 32 bits, four columns a block: thread t has, of block b, column t % 4 of lanes t / 4
 // (register 2 b) and t / 4 + 8 (2 b + 1).  For packed pairs of a K-adjacent operand this is the fragment that a
 // transposed matrix load gives: rows = channels, columns = pairs of tokens.
@@ -128,26 +123,22 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, float* r) {
         : "r"(taddr));
 }
 
-// mbar_wait whose polls let the warp sleep: the warps of this kernel wait for one another much of the time, and
-// the polls of a tight loop were a quarter of all instructions issued.
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int* status) {
+// mbar_wait in few instructions, since the roles' code together has to fit the SM's instruction caches: polls
+// that let the warp sleep (the polls of a tight loop were a quarter of all instructions issued), bounded by their
+// number, at most about two seconds; the caller records a wait that ran out.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
     const uint32_t addr = smem_u32(bar);
-    unsigned long long t0 = 0;
-    while (true) {
+#pragma unroll 1
+    for (int i = 0; i < (1 << 20); ++i) {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
-            : "r"(addr), "r"(parity), "r"(1000000u)   // up to a millisecond a poll
+            : "r"(addr), "r"(parity), "r"(2000u)   // up to two microseconds
             : "memory");
         if (ok) return true;
-        const unsigned long long now = globaltimer();
-        if (!t0) t0 = now;
-        if (now - t0 > kWaitLimitNs) {
-            set_status(status, KDA_ERR_TIMEOUT);
-            return false;
-        }
     }
+    return false;
 }
 
 template <int DK, int DV, bool BOUNDARY>
@@ -159,8 +150,8 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ Decays decays[NST];
-    __shared__ __align__(8) uint64_t full[NST], empty[NST], sp_full, sp_free, p_ready[2], p_free[2], w_ready, z_full,
-        z_free, sb_ready, sb_free, o_full, o_free, done;
+    __shared__ __align__(8) uint64_t full[NST], empty[NST], sp_full, sp_free, p_ready[2], p_free[2], w_ready, z_full[2],
+        z_free[2], sb_ready, sb_free, o_full, o_free, done;
     __shared__ uint32_t tmem_slot;
     const int t = threadIdx.x, w = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
     if (t == 0) {
@@ -173,10 +164,10 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         for (int b = 0; b < 2; ++b) {
             mbar_init(&p_ready[b], kPWarps);
             mbar_init(&p_free[b], 1);
+            mbar_init(&z_full[b], 1);
+            mbar_init(&z_free[b], kSWarps);
         }
         mbar_init(&w_ready, kVWarps);
-        mbar_init(&z_full, 1);
-        mbar_init(&z_free, kSWarps);
         mbar_init(&sb_ready, kSWarps);
         mbar_init(&sb_free, 1);
         mbar_init(&o_full, 1);
@@ -199,7 +190,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
     tc_fence_after();
     const uint32_t tm = tmem_slot;
     const int nch = (it.n + C - 1) / C, hq = h / (a.H / a.Hqk);
-    int* const status = a.status;
+    bool ok = true;   // no wait of this warp has run out
 
     if (w < 4) {
         // every warp of a group of four changes its registers by the same instruction
@@ -218,7 +209,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             int issued = 0;
             for (int c = 0; c < nch; ++c) {
                 const int s = c % NST;
-                if (!bar_wait(&empty[s], ((c / NST) & 1) ^ 1, status)) break;
+                if (!(ok = bar_wait(&empty[s], ((c / NST) & 1) ^ 1))) break;
                 uint8_t* sb = sm + s * F::STAGE;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&full[s], F::STAGE);
@@ -256,7 +247,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     w0 -= lo_f32(part[k]);
                     w1 -= hi_f32(part[k]);
                 }
-                d.w[lane] = make_uint4(part[0], part[1], part[2], 0u);
+                d.w[lane] = make_uint4(part[0], part[1], part[2] ^ 0x80008000u, 0u);
                 if (lane < 16) *reinterpret_cast<float2*>(&d.m[2 * lane]) = make_float2(expf(gm - g0), expf(gm - g1));
                 if (lane == 0) {
                     d.g2m = gm * kLog2e;
@@ -270,64 +261,78 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             }
             if (BOUNDARY && lane == 0) a.zdecay[static_cast<size_t>(it.z0 + it.seg) * a.H + h] = expf(total);
             // no copy stays in flight behind the CTA: wait (bounded, quietly) for the last fill of every stage
-            for (int c = issued > NST ? issued - NST : 0; c < issued; ++c) bar_wait(&full[c % NST], (c / NST) & 1, nullptr);
+    #pragma unroll 1
+        for (int c = issued > NST ? issued - NST : 0; c < issued; ++c) bar_wait(&full[c % NST], (c / NST) & 1);
         } else if (w == 3) {
             // ---------------- issuer
             constexpr uint32_t id_sp = idesc_bf16(128, C), id_o1 = idesc_bf16(128, C),
-                               id_o2 = idesc_bf16(128, C, false, false, true), id_z = idesc_bf16(128, DK, false, true);
+                               id_o2 = idesc_bf16(128, C, false, false, true), id_z = idesc_bf16(128, F::ZN, false, true),
+                               id_zn = idesc_bf16(128, F::ZN, true, true);
             const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0), base = __shfl_sync(0xffffffffu, smem_u32(sm), 0);
             auto scores = [&](int s) {
                 const uint32_t q = base + s * F::STAGE, k = q + F::QB;
                 const uint64_t qd = sdesc_k_sw128(q), kd = sdesc_k_sw128(k);
                 if (elect_one()) {
+#pragma unroll 1
+                    for (int b = 0; b < DK / 64; ++b)
 #pragma unroll
-                    for (int i = 0; i < DK / 16; ++i) {
-                        const uint32_t off = ((i / 4) * F::HALF + (i % 4) * 32) >> 4;
-                        umma_f16(tmu + F::SP, qd + off, kd + off, id_sp, i > 0);
-                    }
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t off = (b * F::HALF + i * 32) >> 4;
+                            umma_f16(tmu + F::SP, qd + off, kd + off, id_sp, b + i > 0);
+                        }
                     umma_commit(&sp_full);
                 }
                 __syncwarp();
             };
-            if (!BOUNDARY && nch > 0 && bar_wait(&full[0], 0, status)) scores(0);
+            if (!BOUNDARY && nch > 0 && (ok = bar_wait(&full[0], 0))) scores(0);
             int s = 0, ph = 0;   // stage of chunk c, and the parity of its use
             for (int c = 0; c < nch; ++c) {
                 const uint32_t q = base + s * F::STAGE, k = q + F::QB, v = k + F::KB;
                 const int s1 = s + 1 == NST ? 0 : s + 1, ph1 = s + 1 == NST ? ph ^ 1 : ph;
-                if (!bar_wait(&full[s], ph, status)) break;
-                if (!bar_wait(&w_ready, c & 1, status)) break;
-                if (c > 0 && !bar_wait(&z_free, (c - 1) & 1, status)) break;
+                if (!(ok = bar_wait(&full[s], ph))) break;
+                if (!(ok = bar_wait(&w_ready, c & 1))) break;
                 tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t kd = sdesc_mn_sw128(k, F::HALF);
+                // 64 channels of k at a time, so that the state warps read one half while the other is formed
 #pragma unroll
-                    for (int p = 0; p < 4; ++p)
+                for (int z = 0; z < DK / F::ZN; ++z) {
+                    if (c > 0) ok = ok && bar_wait(&z_free[z], (c - 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t kd = sdesc_mn_sw128(k + z * (F::ZN / 64) * F::HALF, F::HALF);
+#pragma unroll 1
+                        for (int p = 0; p < 4; ++p)
 #pragma unroll
-                        for (int i = 0; i < C / 16; ++i)
-                            umma_f16_ts(tmu + F::Z, tmu + F::W + 32 * p + 8 * i, kd + i * (2048 >> 4), id_z, p > 0 || i > 0);
-                    umma_commit(&z_full);
+                            for (int i = 0; i < C / 16; ++i)
+                                umma_f16_ts(tmu + F::Z + F::ZN * z, tmu + F::W + 32 * p + 8 * i, kd + i * (2048 >> 4),
+                                            p & 1 ? id_zn : id_z, p > 0 || i > 0);
+                        umma_commit(&z_full[z]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (!ok) break;
                 if (!BOUNDARY) {
                     if (c + 1 < nch) {
-                        if (!bar_wait(&full[s1], ph1, status)) break;
-                        if (!bar_wait(&sp_free, c & 1, status)) break;
+                        if (!(ok = bar_wait(&full[s1], ph1))) break;
+                        if (!(ok = bar_wait(&sp_free, c & 1))) break;
                         tc_fence_after();
                         scores(s1);
                     }
-                    if (!bar_wait(&sb_ready, c & 1, status)) break;
-                    if (c > 0 && !bar_wait(&o_free, (c - 1) & 1, status)) break;
+                    if (!(ok = bar_wait(&sb_ready, c & 1))) break;
+                    if (c > 0 && !(ok = bar_wait(&o_free, (c - 1) & 1))) break;
                     tc_fence_after();
                     if (elect_one()) {
                         const uint64_t qd = sdesc_k_sw128(q);
+#pragma unroll 1
+                        for (int b = 0; b < DK / 64; ++b)
 #pragma unroll
-                        for (int i = 0; i < DK / 16; ++i)
-                            umma_f16_ts(tmu + F::O1, tmu + F::SB + 8 * i, qd + (((i / 4) * F::HALF + (i % 4) * 32) >> 4), id_o1,
-                                        i > 0);
+                            for (int i = 0; i < 4; ++i)
+                                umma_f16_ts(tmu + F::O1, tmu + F::SB + 32 * b + 8 * i, qd + ((b * F::HALF + i * 32) >> 4), id_o1,
+                                            b + i > 0);
                         umma_commit(&sb_free);
                     }
                     __syncwarp();
-                    if (!bar_wait(&p_ready[c & 1], (c >> 1) & 1, status)) break;
+                    if (!(ok = bar_wait(&p_ready[c & 1], (c >> 1) & 1))) break;
                     tc_fence_after();
                     if (elect_one()) {
                         const uint64_t vd = sdesc_mn_sw128(v, F::HALF), pd = sdesc_k_sw128(base + F::P0 + (c & 1) * F::PB);
@@ -346,7 +351,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             }
             if (elect_one()) umma_commit(&done);
             __syncwarp();
-            bar_wait(&done, 0, nullptr);   // no product stays in flight behind the CTA
+            bar_wait(&done, 0);   // no product stays in flight behind the CTA
         } else {
             // ---------------- P: warp w has rows 32 w .. 32 w + 31; columns above the diagonal blocks stay zero
             if (!BOUNDARY) {
@@ -358,52 +363,51 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                             *reinterpret_cast<uint4*>(p0 + b * F::PB + ((i ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
                 for (int c = 0; c < nch; ++c) {
                     const int s = c % NST;
-                    if (!bar_wait(&full[s], (c / NST) & 1, status)) break;
-                    if (!bar_wait(&sp_full, c & 1, status)) break;
+                    if (!(ok = bar_wait(&full[s], (c / NST) & 1))) break;
+                    if (!(ok = bar_wait(&sp_full, c & 1))) break;
                     tc_fence_after();
                     const Decays& d = decays[s];
                     const float gr = d.g2[row];
-                    if (c >= 2 && !bar_wait(&p_free[c & 1], ((c >> 1) - 1) & 1, status)) break;
-                    uint8_t* p = p0 + (c & 1) * F::PB;
                     const uint32_t at = tm + F::SP + (static_cast<uint32_t>(32 * w) << 16);
+                    float x[2][32];
+                    if (w == 1) tmem_ld32(at, x[1]);
+                    tmem_ld32(at + 32 * w, x[0]);
+                    if (w == 1) tmem_wait_ld_regs<32>(x[1]);
+                    tmem_wait_ld_regs<32>(x[0]);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sp_free);
+                    if (c >= 2 && !(ok = bar_wait(&p_free[c & 1], ((c >> 1) - 1) & 1))) break;
+                    uint8_t* p = p0 + (c & 1) * F::PB;
                     auto put = [&](int j0, const uint32_t (&u)[16]) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             *reinterpret_cast<uint4*>(p + (((j0 / 8 + i) ^ (row & 7)) << 4)) =
                                 make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
                     };
-                    float x[32];
                     uint32_t u[16];
                     if (w == 1) {
                         // left of the diagonal block the factor is a product of two, each at most 1, about g_32
-                        tmem_ld32(at, x);
                         const float er = ex2_approx(gr - d.g2m);
-                        tmem_wait_ld_regs<32>(x);
 #pragma unroll
                         for (int j = 0; j < 32; j += 4) {
                             const float4 m = *reinterpret_cast<const float4*>(&d.m[j]);
-                            u[j / 2] = pack_bf16x2(x[j] * (er * m.x), x[j + 1] * (er * m.y));
-                            u[j / 2 + 1] = pack_bf16x2(x[j + 2] * (er * m.z), x[j + 3] * (er * m.w));
+                            u[j / 2] = pack_bf16x2(x[1][j] * (er * m.x), x[1][j + 1] * (er * m.y));
+                            u[j / 2 + 1] = pack_bf16x2(x[1][j + 2] * (er * m.z), x[1][j + 3] * (er * m.w));
                         }
                         put(0, u);
                     }
-                    tmem_ld32(at + 32 * w, x);
-                    tmem_wait_ld_regs<32>(x);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
                         const float4 g = *reinterpret_cast<const float4*>(&d.g2[32 * w + j]);
-                        u[j / 2] = pack_bf16x2(j <= lane ? x[j] * ex2_approx(gr - g.x) : 0.f,
-                                               j + 1 <= lane ? x[j + 1] * ex2_approx(gr - g.y) : 0.f);
-                        u[j / 2 + 1] = pack_bf16x2(j + 2 <= lane ? x[j + 2] * ex2_approx(gr - g.z) : 0.f,
-                                                   j + 3 <= lane ? x[j + 3] * ex2_approx(gr - g.w) : 0.f);
+                        u[j / 2] = pack_bf16x2(j <= lane ? x[0][j] * ex2_approx(gr - g.x) : 0.f,
+                                               j + 1 <= lane ? x[0][j + 1] * ex2_approx(gr - g.y) : 0.f);
+                        u[j / 2 + 1] = pack_bf16x2(j + 2 <= lane ? x[0][j + 2] * ex2_approx(gr - g.z) : 0.f,
+                                                   j + 3 <= lane ? x[0][j + 3] * ex2_approx(gr - g.w) : 0.f);
                     }
                     put(32 * w, u);
-                    tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&sp_free);
-                        mbar_arrive(&empty[s]);
-                    }
+                    if (lane == 0) mbar_arrive(&empty[s]);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&p_ready[c & 1]);
@@ -424,8 +428,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             return (c8 >> 6) * F::HALF + tok * 128 + ((((c8 & 63) >> 3) ^ (tok & 7)) << 4);
         };
         // A wait that runs out ends this warp's work, but not its part in the four warps' own barrier.
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && bar_wait(bar, parity, status); };
+        auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && bar_wait(bar, parity); };
         auto split = [&](int c) {
             const int s = c % NST;
             wait(&full[s], (c / NST) & 1);
@@ -434,6 +437,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             const int n = it.n - c * C;
             if (n < C) {
                 // rows behind the sequence belong to others: they must not reach a sum, not even times zero
+#pragma unroll 1
                 for (int i = tv; ok && i < (C - n) * 8; i += NV) {
                     const int r = n + i / 8, x = r * 128 + (i & 7) * 16;
 #pragma unroll
@@ -444,31 +448,36 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 fence_proxy_async_smem();
                 named_bar_sync(1, NV);
             }
-            if (c > 0) wait(&z_full, (c - 1) & 1);   // W of the chunk before has been read
+            uint32_t u[2][4][8];
             if (mine && ok) {
-                tc_fence_after();
                 const Decays& d = decays[s];
-                uint4 wt[4];   // of this thread's token pair in each block of eight
+                uint4 wt[4];   // of this thread's token pair in each block of eight: w1, w2, -w3
 #pragma unroll
                 for (int b = 0; b < 4; ++b) wt[b] = d.w[half / 2 + 4 * b + (lane & 3)];
 #pragma unroll
                 for (int lh = 0; lh < 2; ++lh) {
-                    uint32_t v[2][4], u[4][8];
+                    uint32_t v[2][4];
                     ldsm_x4_trans(smem_u32(vt) + tile_row(half, lh), v[0]);
                     ldsm_x4_trans(smem_u32(vt) + tile_row(half + 16, lh), v[1]);
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {   // block r / 2, channels 8 (r % 2) + lane / 4 of the sixteen
                         const uint32_t x = v[r >> 2][r & 3];
                         const uint4 wb = wt[r >> 1];
-                        u[0][r] = fma_bf16x2(x, wb.x, 0x80008000u);
-                        u[1][r] = fma_bf16x2(x, wb.x, neg_bf16x2(u[0][r]));
-                        u[2][r] = fma_bf16x2(x, wb.y, 0x80008000u);
-                        u[3][r] = fma_bf16x2(x, wb.z, fma_bf16x2(x, wb.y, neg_bf16x2(u[2][r])));
+                        u[lh][0][r] = fma_bf16x2(x, wb.x, 0x80008000u);
+                        u[lh][1][r] = fma_bf16x2(x, wb.x ^ 0x80008000u, u[lh][0][r]);
+                        u[lh][2][r] = fma_bf16x2(x, wb.y, 0x80008000u);
+                        u[lh][3][r] = fma_bf16x2(x, wb.z, fma_bf16x2(x, wb.y ^ 0x80008000u, u[lh][2][r]));
                     }
+                }
+            }
+            if (c > 0) wait(&z_full[DK / F::ZN - 1], (c - 1) & 1);   // W of the chunk before has been read
+            if (mine && ok) {
+                tc_fence_after();
+#pragma unroll
+                for (int lh = 0; lh < 2; ++lh)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        tmem_st_16x128b_x4(tm + lanes + (static_cast<uint32_t>(16 * lh) << 16) + F::W + 32 * k + half / 2, u[k]);
-                }
+                        tmem_st_16x128b_x4(tm + lanes + (static_cast<uint32_t>(16 * lh) << 16) + F::W + 32 * k + half / 2, u[lh][k]);
                 tmem_wait_st();
                 tc_fence_before();
             }
@@ -532,6 +541,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             } else {   // the rows behind the sequence are not this one's to write
                 __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) +
                                      (static_cast<size_t>(it.t0) + c * C) * a.H * DV + static_cast<size_t>(h) * DV;
+#pragma unroll 1
                 for (int i = tv; ok && i < n * (DV / 8); i += NV) {
                     const int r = i / (DV / 8), k8 = i % (DV / 8);
                     st_global_v4(dst + static_cast<size_t>(r) * a.H * DV + 8 * k8,
@@ -539,11 +549,10 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 }
             }
         };
-        for (int c = 0; c < nch; ++c) {
-            split(c);
+        for (int c = 0; c <= nch; ++c) {
+            if (c < nch) split(c);
             if (!BOUNDARY && c > 0) out(c - 1);
         }
-        if (!BOUNDARY && nch > 0) out(nch - 1);
         if (!BOUNDARY && tv == 0) bulk_wait0();
     } else {
         // ---------------- state: thread = channel of v, S[i] = channel i of k
@@ -575,51 +584,66 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             __syncwarp();
             if (lane == 0) mbar_arrive(&sb_ready);
         };
-        auto store_state = [&](float* dst) {
-            if (mine)
-#pragma unroll
-                for (int i = 0; i < DK; ++i) dst[i * DV + ch] = S[i];
-        };
-        if (!BOUNDARY && nch > 0) publish();
+        float* end = nullptr;
+        if (BOUNDARY) end = a.z + (static_cast<size_t>(it.z0 + it.seg) * a.H + h) * DK * DV;
+        else if (a.final_state && it.seg + 1 == it.n_seg)
+            end = a.final_state + (static_cast<size_t>(it.seq) * a.H + h) * DK * DV;
+        if (nch == 0 && end && mine)   // no tokens: the state stays as it was
+#pragma unroll 1
+            for (int i = 0; i < DK; ++i) end[i * DV + ch] = start ? start[i * DV + ch] : 0.f;
         for (int c = 0; c < nch; ++c) {
             const int s = c % NST;
-            if (!bar_wait(&full[s], (c / NST) & 1, status)) break;
-            const float eC = decays[s].eC;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
-            if (!bar_wait(&z_full, c & 1, status)) break;
-            if (mine) {
-                tc_fence_after();
-#pragma unroll
-                for (int b = 0; b < DK; b += 32) {
-                    float z[32];
-                    tmem_ld32(tm + lanes + F::Z + b, z);
-                    tmem_wait_ld_regs<32>(z);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) S[b + i] = fmaf(eC, S[b + i], z[i]);
-                }
-                tc_fence_before();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&z_free);
-            if (!BOUNDARY && c + 1 < nch) {
-                if (!bar_wait(&sb_free, c & 1, status)) break;
+            if (!BOUNDARY) {
+                if (c > 0 && !(ok = bar_wait(&sb_free, (c - 1) & 1))) break;   // the copy of the chunk before has been read
                 tc_fence_after();
                 publish();
             }
+            if (!(ok = bar_wait(&full[s], (c / NST) & 1))) break;
+            const float eC = decays[s].eC;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);
+#pragma unroll
+            for (int zh = 0; zh < DK / F::ZN; ++zh) {
+                ok = ok && bar_wait(&z_full[zh], c & 1);
+                if (!ok) break;
+                if (mine) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int b = F::ZN * zh; b < F::ZN * (zh + 1); b += 32) {
+                        float z[32];
+                        tmem_ld32(tm + lanes + F::Z + b, z);
+                        tmem_wait_ld_regs<32>(z);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) S[b + i] = fmaf(eC, S[b + i], z[i]);
+                    }
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&z_free[zh]);
+            }
+            if (!ok) break;
+            // a checkpoint, and the state at the segment's end
+            float* dst = nullptr;
             const int pos = it.pos + (c + 1) * C;
             if (!BOUNDARY && a.ckpt_stride && (c + 1) * C <= it.n && pos % a.ckpt_stride == 0) {
                 const long long slot = static_cast<long long>(a.ckpt_cu[it.seq]) + pos / a.ckpt_stride - 1;
                 if (slot >= 0 && slot < a.ckpt_cu[it.seq + 1])
-                    store_state(a.checkpoints + (static_cast<size_t>(slot) * a.H + h) * DK * DV);
+                    dst = a.checkpoints + (static_cast<size_t>(slot) * a.H + h) * DK * DV;
                 else if (lane == 0)
-                    set_status(status, KDA_ERR_DEVICE_INPUT);
+                    set_status(a.status, KDA_ERR_DEVICE_INPUT);
+            }
+            if (mine && (dst || (end && c + 1 == nch))) {
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) {
+                    float* p = k == 0 ? dst : c + 1 == nch ? end : nullptr;
+                    if (p)
+#pragma unroll
+                        for (int i = 0; i < DK; ++i) p[i * DV + ch] = S[i];
+                }
             }
         }
-        if (BOUNDARY) store_state(a.z + (static_cast<size_t>(it.z0 + it.seg) * a.H + h) * DK * DV);
-        else if (a.final_state && it.seg + 1 == it.n_seg)
-            store_state(a.final_state + (static_cast<size_t>(it.seq) * a.H + h) * DK * DV);
     }
+    if (!ok && lane == 0) set_status(a.status, KDA_ERR_TIMEOUT);
     tc_fence_before();
     __syncthreads();
     if (w == 3) tmem_dealloc(tm, F::COLS);
