@@ -49,7 +49,6 @@ struct Cfg {
     static constexpr uint32_t P0 = NST * STAGE, O0 = P0 + (BOUNDARY ? 0 : 2 * PB);
     // the A operands of 128 rows read past 64-row tiles (their results are not used): the tiles behind exist
     static constexpr uint32_t BYTES = O0 + (BOUNDARY ? HALF : 2 * VB);
-    static constexpr int ZN = DK;   // channels of k that one piece of Z has
     // tensor memory columns
     static constexpr uint32_t SP = 0, O1 = 64, O2 = 128, Z = 192, SB = 320, W = 384, COLS = 512;   // W: 4 x 32
     static_assert(BYTES + 1024 + 4096 <= 227 * 1024, "shared memory");
@@ -74,13 +73,27 @@ struct Decays {            // of one chunk
 __device__ __forceinline__ float lo_f32(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
-// One lane of a converged warp, always the same one.  The MMAs are issued under this predicate by a warp whose
-// addresses are warp-uniform values: issued by a lane chosen with threadIdx, from values the compiler cannot
-// see to be uniform, each costs about 96 cycles; so, 32 to 64 (M = 128, K = 16, N = 64 to 128).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t e;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-    return e != 0;
+// MMAs for a whole converged warp, issued by its elected lane, with warp-uniform operands.  Issued by a lane
+// chosen with threadIdx, from values the compiler cannot see to be uniform, each costs about 96 cycles; so, 32 to
+// 64 (M = 128, K = 16, N = 64 to 128).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Commits what the elected lane has issued.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
 }
 
 // 32 consecutive columns of this warp's lanes
@@ -123,22 +136,21 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, float* r) {
         : "r"(taddr));
 }
 
-// mbar_wait in few instructions, since the roles' code together has to fit the SM's instruction caches: polls
-// that let the warp sleep (the polls of a tight loop were a quarter of all instructions issued), bounded by their
-// number, at most about two seconds; the caller records a wait that ran out.
+// mbar_wait in few instructions, since the roles' code together has to fit the SM's instruction caches (see the
+// kernel): polls that let the warp sleep for a while, bounded by their number; the caller records a wait that
+// ran out.
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
-    const uint32_t addr = smem_u32(bar);
 #pragma unroll 1
-    for (int i = 0; i < (1 << 20); ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(addr), "r"(parity), "r"(2000u)   // up to two microseconds
-            : "memory");
-        if (ok) return true;
-    }
+    for (int i = 0; i < (1 << 22); ++i)
+        if (mbar_try_wait(bar, parity)) return true;
     return false;
+}
+
+// e^x for x <= 0 to about one unit in the last place: 2^(x log2 e) with the rounding of the product put back.
+__device__ __forceinline__ float exp_fast(float x) {
+    const float y = x * kLog2e, r = fmaf(x, kLog2e, -y) + x * 1.9259629e-8f;   // log2(e) - kLog2e
+    const float e = ex2_approx(y);
+    return fmaf(e, r * 0.69314718f, e);
 }
 
 template <int DK, int DV, bool BOUNDARY>
@@ -150,8 +162,8 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ Decays decays[NST];
-    __shared__ __align__(8) uint64_t full[NST], empty[NST], sp_full, sp_free, p_ready[2], p_free[2], w_ready, z_full[2],
-        z_free[2], sb_ready, sb_free, o_full, o_free, done;
+    __shared__ __align__(8) uint64_t full[NST], empty[NST], sp_full, sp_free, p_ready[2], p_free[2], z_go, z_full,
+        o_go, sb_free, o_full, done;
     __shared__ uint32_t tmem_slot;
     const int t = threadIdx.x, w = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
     if (t == 0) {
@@ -164,14 +176,12 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         for (int b = 0; b < 2; ++b) {
             mbar_init(&p_ready[b], kPWarps);
             mbar_init(&p_free[b], 1);
-            mbar_init(&z_full[b], 1);
-            mbar_init(&z_free[b], kSWarps);
         }
-        mbar_init(&w_ready, kVWarps);
-        mbar_init(&sb_ready, kSWarps);
+        mbar_init(&z_go, kVWarps + kSWarps);    // W is in place, and Z of the chunk before has been read
+        mbar_init(&z_full, 1);
+        mbar_init(&o_go, kVWarps + kSWarps);    // Sb is in place, and O1, O2 of the chunk before have been read
         mbar_init(&sb_free, 1);
         mbar_init(&o_full, 1);
-        mbar_init(&o_free, kVWarps);
         mbar_init(&done, 1);
         fence_barrier_init();
     }
@@ -197,35 +207,38 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (w == 2) {
             // ---------------- producer
-            const float* la = a.la + static_cast<size_t>(h) * a.la_h;
-            auto log_alpha = [&](int c, float& x0, float& x1) {
-                const int i = c * C + 2 * lane;
-                const size_t tok = static_cast<size_t>(it.t0) + i;
-                x0 = i < it.n ? fmaxf(la[tok * a.la_t], kLinLogMin) : 0.f;
-                x1 = i + 1 < it.n ? fmaxf(la[(tok + 1) * a.la_t], kLinLogMin) : 0.f;
+            // this lane's tokens 2 lane and 2 lane + 1 of the chunk
+            const float* la = a.la + (static_cast<size_t>(it.t0) + 2 * lane) * a.la_t + h;
+            int left = it.n - 2 * lane;   // tokens of the segment from the lane's first one on
+            auto log_alpha = [&](float& x0, float& x1) {
+                x0 = left > 0 ? fmaxf(la[0], kLinLogMin) : 0.f;
+                x1 = left > 1 ? fmaxf(la[a.la_t], kLinLogMin) : 0.f;
+                la += C * static_cast<size_t>(a.la_t);
+                left -= C;
             };
             float x0, x1, total = 0.f;
-            if (nch > 0) log_alpha(0, x0, x1);
-            int issued = 0;
+            log_alpha(x0, x1);
+            int s = 0, ph = 1, issued = 0;
+#pragma unroll 1
             for (int c = 0; c < nch; ++c) {
-                const int s = c % NST;
-                if (!(ok = bar_wait(&empty[s], ((c / NST) & 1) ^ 1))) break;
-                uint8_t* sb = sm + s * F::STAGE;
+                if (!(ok = bar_wait(&empty[s], ph))) break;
                 if (lane == 0) {
+                    uint8_t* sb = sm + s * F::STAGE;
                     mbar_arrive_expect_tx(&full[s], F::STAGE);
                     const int tok = it.t0 + c * C;
-                    if (!BOUNDARY)
-                        for (int b = 0; b < DK / 64; ++b) tma_load_2d(sb + b * F::HALF, &mq, hq * DK + 64 * b, tok, &full[s]);
-                    for (int b = 0; b < DK / 64; ++b) tma_load_2d(sb + F::QB + b * F::HALF, &mk, hq * DK + 64 * b, tok, &full[s]);
+#pragma unroll 1
+                    for (int b = 0; b < DK / 64; ++b) {
+                        if (!BOUNDARY) tma_load_2d(sb + b * F::HALF, &mq, hq * DK + 64 * b, tok, &full[s]);
+                        tma_load_2d(sb + F::QB + b * F::HALF, &mk, hq * DK + 64 * b, tok, &full[s]);
+                    }
+#pragma unroll 1
                     for (int b = 0; b < DV / 64; ++b)
                         tma_load_2d(sb + F::QB + F::KB + b * F::HALF, &mv, h * DV + 64 * b, tok, &full[s]);
                 }
                 issued = c + 1;
                 // inclusive sums of the lanes' pairs, from the chunk's start and from its end
-                float y0 = 0.f, y1 = 0.f;
-                if (c + 1 < nch) log_alpha(c + 1, y0, y1);
                 float f = x0 + x1, r = f;
-#pragma unroll
+#pragma unroll 1
                 for (int off = 1; off < 32; off <<= 1) {
                     const float u = __shfl_up_sync(0xffffffffu, f, off), v = __shfl_down_sync(0xffffffffu, r, off);
                     if (lane >= off) f += u;
@@ -234,12 +247,12 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 float before = __shfl_up_sync(0xffffffffu, f, 1), after = __shfl_down_sync(0xffffffffu, r, 1);
                 if (lane == 0) before = 0.f;
                 if (lane == 31) after = 0.f;
-                const float sum = __shfl_sync(0xffffffffu, f, 31);
+                const float sum = __shfl_sync(0xffffffffu, f, 31), gm = __shfl_sync(0xffffffffu, f, 15);
                 Decays& d = decays[s];
-                const float g0 = before + x0, g1 = f, gm = __shfl_sync(0xffffffffu, f, 15);
-                *reinterpret_cast<float2*>(&d.g2[2 * lane]) = make_float2(g0 * kLog2e, g1 * kLog2e);
-                *reinterpret_cast<float2*>(&d.eg[2 * lane]) = make_float2(expf(g0), expf(g1));
-                float w0 = expf(after + x1), w1 = expf(after);
+                const float2 g = make_float2(before + x0, f);
+                *reinterpret_cast<float2*>(&d.g2[2 * lane]) = make_float2(g.x * kLog2e, g.y * kLog2e);
+                *reinterpret_cast<float2*>(&d.eg[2 * lane]) = make_float2(exp_fast(g.x), exp_fast(g.y));
+                float w0 = exp_fast(after + x1), w1 = exp_fast(after);
                 uint32_t part[3];
 #pragma unroll
                 for (int k = 0; k < 3; ++k) {
@@ -248,110 +261,83 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     w1 -= hi_f32(part[k]);
                 }
                 d.w[lane] = make_uint4(part[0], part[1], part[2] ^ 0x80008000u, 0u);
-                if (lane < 16) *reinterpret_cast<float2*>(&d.m[2 * lane]) = make_float2(expf(gm - g0), expf(gm - g1));
+                if (lane < 16)
+                    *reinterpret_cast<float2*>(&d.m[2 * lane]) =
+                        make_float2(ex2_approx((gm - g.x) * kLog2e), ex2_approx((gm - g.y) * kLog2e));
                 if (lane == 0) {
                     d.g2m = gm * kLog2e;
-                    d.eC = expf(sum);
+                    d.eC = exp_fast(sum);
                 }
                 total += sum;
-                x0 = y0;
-                x1 = y1;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[s]);
+                log_alpha(x0, x1);   // of the next chunk
+                if (++s == NST) {
+                    s = 0;
+                    ph ^= 1;
+                }
             }
-            if (BOUNDARY && lane == 0) a.zdecay[static_cast<size_t>(it.z0 + it.seg) * a.H + h] = expf(total);
+            if (BOUNDARY && lane == 0) a.zdecay[static_cast<size_t>(it.z0 + it.seg) * a.H + h] = exp_fast(total);
             // no copy stays in flight behind the CTA: wait (bounded, quietly) for the last fill of every stage
     #pragma unroll 1
         for (int c = issued > NST ? issued - NST : 0; c < issued; ++c) bar_wait(&full[c % NST], (c / NST) & 1);
         } else if (w == 3) {
             // ---------------- issuer
-            constexpr uint32_t id_sp = idesc_bf16(128, C), id_o1 = idesc_bf16(128, C),
-                               id_o2 = idesc_bf16(128, C, false, false, true), id_z = idesc_bf16(128, F::ZN, false, true),
-                               id_zn = idesc_bf16(128, F::ZN, true, true);
+            constexpr uint32_t id_o = idesc_bf16(128, C), id_o2 = idesc_bf16(128, C, false, false, true),
+                               id_z = idesc_bf16(128, DK, false, true), neg_a = 1u << 13;
             const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0), base = __shfl_sync(0xffffffffu, smem_u32(sm), 0);
+            // K = 16 slice i of a K-major tile of 64-channel halves, in descriptor units
+            auto slice = [](int i) { return static_cast<uint32_t>((i >> 2) * (F::HALF >> 4) + (i & 3) * 2); };
             auto scores = [&](int s) {
                 const uint32_t q = base + s * F::STAGE, k = q + F::QB;
                 const uint64_t qd = sdesc_k_sw128(q), kd = sdesc_k_sw128(k);
-                if (elect_one()) {
-#pragma unroll 1
-                    for (int b = 0; b < DK / 64; ++b)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t off = (b * F::HALF + i * 32) >> 4;
-                            umma_f16(tmu + F::SP, qd + off, kd + off, id_sp, b + i > 0);
-                        }
-                    umma_commit(&sp_full);
-                }
-                __syncwarp();
+                for (int i = 0; i < DK / 16; ++i) mma_ss(tmu + F::SP, qd + slice(i), kd + slice(i), id_o, i > 0);
+                mma_commit(&sp_full);
             };
             if (!BOUNDARY && nch > 0 && (ok = bar_wait(&full[0], 0))) scores(0);
             int s = 0, ph = 0;   // stage of chunk c, and the parity of its use
-            for (int c = 0; c < nch; ++c) {
+#pragma unroll 1
+            for (int c = 0; ok && c < nch; ++c) {
                 const uint32_t q = base + s * F::STAGE, k = q + F::QB, v = k + F::KB;
                 const int s1 = s + 1 == NST ? 0 : s + 1, ph1 = s + 1 == NST ? ph ^ 1 : ph;
-                if (!(ok = bar_wait(&full[s], ph))) break;
-                if (!(ok = bar_wait(&w_ready, c & 1))) break;
+                if (BOUNDARY && !(ok = bar_wait(&full[s], ph))) break;
+                if (!(ok = bar_wait(&z_go, c & 1))) break;
                 tc_fence_after();
-                // 64 channels of k at a time, so that the state warps read one half while the other is formed
-#pragma unroll
-                for (int z = 0; z < DK / F::ZN; ++z) {
-                    if (c > 0) ok = ok && bar_wait(&z_free[z], (c - 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t kd = sdesc_mn_sw128(k + z * (F::ZN / 64) * F::HALF, F::HALF);
+                const uint64_t kd = sdesc_mn_sw128(k, F::HALF);
 #pragma unroll 1
-                        for (int p = 0; p < 4; ++p)
-#pragma unroll
-                            for (int i = 0; i < C / 16; ++i)
-                                umma_f16_ts(tmu + F::Z + F::ZN * z, tmu + F::W + 32 * p + 8 * i, kd + i * (2048 >> 4),
-                                            p & 1 ? id_zn : id_z, p > 0 || i > 0);
-                        umma_commit(&z_full[z]);
-                    }
-                    __syncwarp();
-                }
-                if (!ok) break;
+                for (int i = 0; i < 16; ++i)   // part i / 4, tokens 16 (i % 4) ..; the odd parts are negated
+                    mma_ts(tmu + F::Z, tmu + F::W + 8 * i, kd + (i & 3) * (2048 >> 4), id_z | ((i & 4) ? neg_a : 0u),
+                                i > 0);
+                mma_commit(&z_full);
                 if (!BOUNDARY) {
                     if (c + 1 < nch) {
-                        if (!(ok = bar_wait(&full[s1], ph1))) break;
-                        if (!(ok = bar_wait(&sp_free, c & 1))) break;
+                        if (!(ok = bar_wait(&full[s1], ph1) && bar_wait(&sp_free, c & 1))) break;
                         tc_fence_after();
                         scores(s1);
                     }
-                    if (!(ok = bar_wait(&sb_ready, c & 1))) break;
-                    if (c > 0 && !(ok = bar_wait(&o_free, (c - 1) & 1))) break;
+                    if (!(ok = bar_wait(&o_go, c & 1))) break;
                     tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t qd = sdesc_k_sw128(q);
-#pragma unroll 1
-                        for (int b = 0; b < DK / 64; ++b)
+                    const uint64_t qd = sdesc_k_sw128(q);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                umma_f16_ts(tmu + F::O1, tmu + F::SB + 32 * b + 8 * i, qd + ((b * F::HALF + i * 32) >> 4), id_o1,
-                                            b + i > 0);
-                        umma_commit(&sb_free);
-                    }
-                    __syncwarp();
+                    for (int i = 0; i < DK / 16; ++i) mma_ts(tmu + F::O1, tmu + F::SB + 8 * i, qd + slice(i), id_o, i > 0);
+                    mma_commit(&sb_free);
                     if (!(ok = bar_wait(&p_ready[c & 1], (c >> 1) & 1))) break;
                     tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t vd = sdesc_mn_sw128(v, F::HALF), pd = sdesc_k_sw128(base + F::P0 + (c & 1) * F::PB);
+                    const uint64_t vd = sdesc_mn_sw128(v, F::HALF), pd = sdesc_k_sw128(base + F::P0 + (c & 1) * F::PB);
 #pragma unroll
-                        for (int i = 0; i < C / 16; ++i)
-                            umma_f16(tmu + F::O2, vd + i * (2048 >> 4), pd + i * (32 >> 4), id_o2, i > 0);
-                        umma_commit(&o_full);
-                        umma_commit(&p_free[c & 1]);
-                    }
-                    __syncwarp();
+                    for (int i = 0; i < C / 16; ++i) mma_ss(tmu + F::O2, vd + i * (2048 >> 4), pd + i * 2, id_o2, i > 0);
+                    mma_commit(&o_full);
+                    mma_commit(&p_free[c & 1]);
+                    mma_commit(&empty[s]);
+                } else {
+                    mma_commit(&empty[s]);
                 }
-                if (elect_one()) umma_commit(&empty[s]);
-                __syncwarp();
                 s = s1;
                 ph = ph1;
             }
-            if (elect_one()) umma_commit(&done);
-            __syncwarp();
-            bar_wait(&done, 0);   // no product stays in flight behind the CTA
+            mma_commit(&done);
+            ok = bar_wait(&done, 0) && ok;   // no product stays in flight behind the CTA
         } else {
             // ---------------- P: warp w has rows 32 w .. 32 w + 31; columns above the diagonal blocks stay zero
             if (!BOUNDARY) {
@@ -361,56 +347,69 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     for (int b = 0; b < 2; ++b)
                         for (int i = 4; i < 8; ++i)
                             *reinterpret_cast<uint4*>(p0 + b * F::PB + ((i ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                auto put = [&](uint8_t* p, int j0, const uint32_t (&u)[8]) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        *reinterpret_cast<uint4*>(p + (((j0 / 8 + i) ^ (row & 7)) << 4)) =
+                            make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+                };
+                int s = 0, ph = 0;
+#pragma unroll 1
                 for (int c = 0; c < nch; ++c) {
-                    const int s = c % NST;
-                    if (!(ok = bar_wait(&full[s], (c / NST) & 1))) break;
-                    if (!(ok = bar_wait(&sp_full, c & 1))) break;
+                    if (!(ok = bar_wait(&full[s], ph) && bar_wait(&sp_full, c & 1))) break;
                     tc_fence_after();
                     const Decays& d = decays[s];
                     const float gr = d.g2[row];
                     const uint32_t at = tm + F::SP + (static_cast<uint32_t>(32 * w) << 16);
-                    float x[2][32];
-                    if (w == 1) tmem_ld32(at, x[1]);
-                    tmem_ld32(at + 32 * w, x[0]);
-                    if (w == 1) tmem_wait_ld_regs<32>(x[1]);
-                    tmem_wait_ld_regs<32>(x[0]);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sp_free);
                     if (c >= 2 && !(ok = bar_wait(&p_free[c & 1], ((c >> 1) - 1) & 1))) break;
                     uint8_t* p = p0 + (c & 1) * F::PB;
-                    auto put = [&](int j0, const uint32_t (&u)[16]) {
+                    // sixteen columns a turn: left of the diagonal block (second warp) the factor is a product of
+                    // two, each at most 1, about g_32
+                    const float er = ex2_approx(gr - d.g2m);
+#pragma unroll 1
+                    for (int j0 = 0; j0 < 32 * w; j0 += 16) {
+                        float x[16];
+                        uint32_t u[8];
+                        tmem_ld16(at + j0, x);
+                        tmem_wait_ld_regs<16>(x);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            *reinterpret_cast<uint4*>(p + (((j0 / 8 + i) ^ (row & 7)) << 4)) =
-                                make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
-                    };
-                    uint32_t u[16];
-                    if (w == 1) {
-                        // left of the diagonal block the factor is a product of two, each at most 1, about g_32
-                        const float er = ex2_approx(gr - d.g2m);
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 m = *reinterpret_cast<const float4*>(&d.m[j]);
-                            u[j / 2] = pack_bf16x2(x[1][j] * (er * m.x), x[1][j + 1] * (er * m.y));
-                            u[j / 2 + 1] = pack_bf16x2(x[1][j + 2] * (er * m.z), x[1][j + 3] * (er * m.w));
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 m = *reinterpret_cast<const float4*>(&d.m[j0 + j]);
+                            u[j / 2] = pack_bf16x2(x[j] * (er * m.x), x[j + 1] * (er * m.y));
+                            u[j / 2 + 1] = pack_bf16x2(x[j + 2] * (er * m.z), x[j + 3] * (er * m.w));
                         }
-                        put(0, u);
+                        put(p, j0, u);
                     }
+#pragma unroll 1
+                    for (int j0 = 32 * w; j0 < 32 * w + 32; j0 += 16) {
+                        float x[16];
+                        uint32_t u[8];
+                        tmem_ld16(at + j0, x);
+                        tmem_wait_ld_regs<16>(x);
+                        const int k = row - j0;   // the row's own column
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 g = *reinterpret_cast<const float4*>(&d.g2[32 * w + j]);
-                        u[j / 2] = pack_bf16x2(j <= lane ? x[0][j] * ex2_approx(gr - g.x) : 0.f,
-                                               j + 1 <= lane ? x[0][j + 1] * ex2_approx(gr - g.y) : 0.f);
-                        u[j / 2 + 1] = pack_bf16x2(j + 2 <= lane ? x[0][j + 2] * ex2_approx(gr - g.z) : 0.f,
-                                                   j + 3 <= lane ? x[0][j + 3] * ex2_approx(gr - g.w) : 0.f);
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 g = *reinterpret_cast<const float4*>(&d.g2[j0 + j]);
+                            u[j / 2] = pack_bf16x2(j <= k ? x[j] * ex2_approx(gr - g.x) : 0.f,
+                                                   j + 1 <= k ? x[j + 1] * ex2_approx(gr - g.y) : 0.f);
+                            u[j / 2 + 1] = pack_bf16x2(j + 2 <= k ? x[j + 2] * ex2_approx(gr - g.z) : 0.f,
+                                                       j + 3 <= k ? x[j + 3] * ex2_approx(gr - g.w) : 0.f);
+                        }
+                        put(p, j0, u);
                     }
-                    put(32 * w, u);
+                    tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&empty[s]);
+                    if (lane == 0) {
+                        mbar_arrive(&sp_free);
+                        mbar_arrive(&empty[s]);
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&p_ready[c & 1]);
+                    if (++s == NST) {
+                        s = 0;
+                        ph ^= 1;
+                    }
                 }
             }
         }
@@ -448,42 +447,37 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 fence_proxy_async_smem();
                 named_bar_sync(1, NV);
             }
-            uint32_t u[2][4][8];
+            if (c > 0) wait(&z_full, (c - 1) & 1);   // W of the chunk before has been read
             if (mine && ok) {
+                tc_fence_after();
                 const Decays& d = decays[s];
                 uint4 wt[4];   // of this thread's token pair in each block of eight: w1, w2, -w3
 #pragma unroll
                 for (int b = 0; b < 4; ++b) wt[b] = d.w[half / 2 + 4 * b + (lane & 3)];
-#pragma unroll
+#pragma unroll 1
                 for (int lh = 0; lh < 2; ++lh) {
-                    uint32_t v[2][4];
+                    uint32_t v[2][4], u[4][8];
                     ldsm_x4_trans(smem_u32(vt) + tile_row(half, lh), v[0]);
                     ldsm_x4_trans(smem_u32(vt) + tile_row(half + 16, lh), v[1]);
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {   // block r / 2, channels 8 (r % 2) + lane / 4 of the sixteen
                         const uint32_t x = v[r >> 2][r & 3];
                         const uint4 wb = wt[r >> 1];
-                        u[lh][0][r] = fma_bf16x2(x, wb.x, 0x80008000u);
-                        u[lh][1][r] = fma_bf16x2(x, wb.x ^ 0x80008000u, u[lh][0][r]);
-                        u[lh][2][r] = fma_bf16x2(x, wb.y, 0x80008000u);
-                        u[lh][3][r] = fma_bf16x2(x, wb.z, fma_bf16x2(x, wb.y ^ 0x80008000u, u[lh][2][r]));
+                        u[0][r] = fma_bf16x2(x, wb.x, 0x80008000u);
+                        u[1][r] = fma_bf16x2(x, wb.x ^ 0x80008000u, u[0][r]);
+                        u[2][r] = fma_bf16x2(x, wb.y, 0x80008000u);
+                        u[3][r] = fma_bf16x2(x, wb.z, fma_bf16x2(x, wb.y ^ 0x80008000u, u[2][r]));
                     }
-                }
-            }
-            if (c > 0) wait(&z_full[DK / F::ZN - 1], (c - 1) & 1);   // W of the chunk before has been read
-            if (mine && ok) {
-                tc_fence_after();
-#pragma unroll
-                for (int lh = 0; lh < 2; ++lh)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        tmem_st_16x128b_x4(tm + lanes + (static_cast<uint32_t>(16 * lh) << 16) + F::W + 32 * k + half / 2, u[lh][k]);
+                        tmem_st_16x128b_x4(tm + lanes + (static_cast<uint32_t>(16 * lh) << 16) + F::W + 32 * k + half / 2, u[k]);
+                }
                 tmem_wait_st();
                 tc_fence_before();
             }
             __syncwarp();
             if (lane == 0 && ok) {
-                mbar_arrive(&w_ready);
+                mbar_arrive(&z_go);
                 if (BOUNDARY) mbar_arrive(&empty[s]);
             }
         };
@@ -497,20 +491,17 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             if (mine && ok) {
                 tc_fence_after();
                 const Decays& d = decays[s];
-                float x[2][16], y[2][16];
-#pragma unroll
-                for (int lh = 0; lh < 2; ++lh) {
-                    const uint32_t at = tm + lanes + (static_cast<uint32_t>(16 * lh) << 16) + half;
-                    tmem_ld_16x256b_x4(at + F::O1, x[lh]);
-                    tmem_ld_16x256b_x4(at + F::O2, y[lh]);
-                }
                 float2 e[4];
 #pragma unroll
                 for (int b = 0; b < 4; ++b) e[b] = *reinterpret_cast<const float2*>(&d.eg[half + 8 * b + 2 * (lane & 3)]);
-#pragma unroll
+#pragma unroll 1
                 for (int lh = 0; lh < 2; ++lh) {
-                    tmem_wait_ld_regs<16>(x[lh]);
-                    tmem_wait_ld_regs<16>(y[lh]);
+                    float x[16], y[16];
+                    const uint32_t at = tm + lanes + (static_cast<uint32_t>(16 * lh) << 16) + half;
+                    tmem_ld_16x256b_x4(at + F::O1, x);
+                    tmem_ld_16x256b_x4(at + F::O2, y);
+                    tmem_wait_ld_regs<16>(x);
+                    tmem_wait_ld_regs<16>(y);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         uint32_t u[4];
@@ -518,7 +509,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         for (int r = 0; r < 4; ++r) {   // block 2 i + r / 2, channels 8 (r % 2) + lane / 4
                             const int k = 8 * i + 2 * r;
                             const float2 eb = e[2 * i + (r >> 1)];
-                            u[r] = pack_bf16x2(fmaf(eb.x, x[lh][k], y[lh][k]), fmaf(eb.y, x[lh][k + 1], y[lh][k + 1]));
+                            u[r] = pack_bf16x2(fmaf(eb.x, x[k], y[k]), fmaf(eb.y, x[k + 1], y[k + 1]));
                         }
                         stsm_x4_trans(smem_u32(ob) + tile_row(half + 16 * i, lh), u);
                     }
@@ -528,7 +519,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0 && ok) {
-                mbar_arrive(&o_free);
+                mbar_arrive(&o_go);
                 mbar_arrive(&empty[s]);
             }
             named_bar_sync(1, NV);
@@ -549,6 +540,8 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 }
             }
         };
+        if (lane == 0) mbar_arrive(&o_go);   // there is no o before the first
+#pragma unroll 1
         for (int c = 0; c <= nch; ++c) {
             if (c < nch) split(c);
             if (!BOUNDARY && c > 0) out(c - 1);
@@ -569,6 +562,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         }
 #pragma unroll
         for (int i = 0; i < DK; ++i) S[i] = start && mine ? start[i * DV + ch] : 0.f;
+        if (lane == 0) mbar_arrive(&z_go);   // there is no Z before the first
         auto publish = [&]() {   // the bf16 copy that O1 multiplies q with
             if (mine) {
 #pragma unroll
@@ -582,7 +576,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 tc_fence_before();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sb_ready);
+            if (lane == 0) mbar_arrive(&o_go);
         };
         float* end = nullptr;
         if (BOUNDARY) end = a.z + (static_cast<size_t>(it.z0 + it.seg) * a.H + h) * DK * DV;
@@ -591,46 +585,53 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         if (nch == 0 && end && mine)   // no tokens: the state stays as it was
 #pragma unroll 1
             for (int i = 0; i < DK; ++i) end[i * DV + ch] = start ? start[i * DV + ch] : 0.f;
+        // tokens to the next checkpoint, and its place
+        int to_ck = 0x7fffffff, ck = 0;
+        if (!BOUNDARY && a.ckpt_stride) {
+            to_ck = a.ckpt_stride - it.pos % a.ckpt_stride;
+            ck = a.ckpt_cu[it.seq] + it.pos / a.ckpt_stride;
+        }
+        int s = 0, ph = 0;
+#pragma unroll 1
         for (int c = 0; c < nch; ++c) {
-            const int s = c % NST;
             if (!BOUNDARY) {
                 if (c > 0 && !(ok = bar_wait(&sb_free, (c - 1) & 1))) break;   // the copy of the chunk before has been read
                 tc_fence_after();
                 publish();
             }
-            if (!(ok = bar_wait(&full[s], (c / NST) & 1))) break;
+            if (!(ok = bar_wait(&full[s], ph))) break;
             const float eC = decays[s].eC;
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
+            if (!(ok = bar_wait(&z_full, c & 1))) break;
+            if (mine) {
+                tc_fence_after();
 #pragma unroll
-            for (int zh = 0; zh < DK / F::ZN; ++zh) {
-                ok = ok && bar_wait(&z_full[zh], c & 1);
-                if (!ok) break;
-                if (mine) {
-                    tc_fence_after();
+                for (int b = 0; b < DK; b += 32) {
+                    float z[32];
+                    tmem_ld32(tm + lanes + F::Z + b, z);
+                    tmem_wait_ld_regs<32>(z);
 #pragma unroll
-                    for (int b = F::ZN * zh; b < F::ZN * (zh + 1); b += 32) {
-                        float z[32];
-                        tmem_ld32(tm + lanes + F::Z + b, z);
-                        tmem_wait_ld_regs<32>(z);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) S[b + i] = fmaf(eC, S[b + i], z[i]);
-                    }
-                    tc_fence_before();
+                    for (int i = 0; i < 32; ++i) S[b + i] = fmaf(eC, S[b + i], z[i]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&z_free[zh]);
+                tc_fence_before();
             }
-            if (!ok) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&z_go);
             // a checkpoint, and the state at the segment's end
             float* dst = nullptr;
-            const int pos = it.pos + (c + 1) * C;
-            if (!BOUNDARY && a.ckpt_stride && (c + 1) * C <= it.n && pos % a.ckpt_stride == 0) {
-                const long long slot = static_cast<long long>(a.ckpt_cu[it.seq]) + pos / a.ckpt_stride - 1;
-                if (slot >= 0 && slot < a.ckpt_cu[it.seq + 1])
-                    dst = a.checkpoints + (static_cast<size_t>(slot) * a.H + h) * DK * DV;
+            to_ck -= C;
+            if (!BOUNDARY && to_ck == 0 && (c + 1) * C <= it.n) {
+                to_ck = a.ckpt_stride;
+                if (ck >= 0 && ck < a.ckpt_cu[it.seq + 1])
+                    dst = a.checkpoints + (static_cast<size_t>(ck) * a.H + h) * DK * DV;
                 else if (lane == 0)
                     set_status(a.status, KDA_ERR_DEVICE_INPUT);
+                ++ck;
+            }
+            if (++s == NST) {
+                s = 0;
+                ph ^= 1;
             }
             if (mine && (dst || (end && c + 1 == nch))) {
 #pragma unroll 1
