@@ -20,7 +20,7 @@
 //
 // The warps are specialised and meet at mbarriers: a producer (TMA tiles of q, k, v, and the chunk's decays),
 // an issuer (all MMAs, in an order that keeps Z of one chunk ahead of the scores of the next), two warps for
-// P, eight that split W and write o, four that hold the state.
+// P, four that split W, four that write o, four that hold the state.
 #include <string.h>
 
 #include "kda_device.cuh"
@@ -50,11 +50,14 @@ struct Cfg {
     // the A operands of 128 rows read past 64-row tiles (their results are not used): the tiles behind exist
     static constexpr uint32_t BYTES = O0 + (BOUNDARY ? HALF : 2 * VB);
     // tensor memory columns
-    static constexpr uint32_t SP = 0, O1 = 64, O2 = 128, Z = 192, SB = 320, W = 384, COLS = 512;   // W: 4 x 32
+    // (W: 4 x 32; the boundary pass has room for Z twice: chunk c uses place c % NZ)
+    static constexpr uint32_t SP = 0, O1 = 64, O2 = 128, SB = 320, W = 384, COLS = 512;
+    static constexpr int NZ = BOUNDARY ? 2 : 1;
+    static constexpr uint32_t Z = BOUNDARY ? 0 : 192;
     static_assert(BYTES + 1024 + 4096 <= 227 * 1024, "shared memory");
 };
 constexpr int kThreads = 512;
-constexpr int kPWarps = 2, kVWarps = 8, kSWarps = 4;
+constexpr int kPWarps = 2, kWWarps = 4, kOWarps = 4, kSWarps = 4;
 // Registers of a thread: 128 at launch; the warps that hold the state take 176, the others give theirs
 // (3 x 112 + 176 = 512, what four threads of the four groups were launched with).
 constexpr int kRegsState = 176, kRegsOther = 112;
@@ -162,24 +165,26 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ Decays decays[NST];
-    __shared__ __align__(8) uint64_t full[NST], empty[NST], sp_full, sp_free, p_ready[2], p_free[2], z_go, z_full,
-        o_go, sb_free, o_full, done;
+    __shared__ __align__(8) uint64_t full[NST], empty[NST], sp_full, sp_free, p_ready[2], p_free[2], w_go[2], w_free[2], z_free[2],
+        z_full[2], o_go, sb_free, o_full, done;
     __shared__ uint32_t tmem_slot;
     const int t = threadIdx.x, w = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
     if (t == 0) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(&full[s], 2);
-            mbar_init(&empty[s], 1 + (BOUNDARY ? 0 : kPWarps) + kVWarps + kSWarps);
+            mbar_init(&empty[s], 1 + kWWarps + kSWarps + (BOUNDARY ? 0 : kPWarps + kOWarps));
         }
         mbar_init(&sp_full, 1);
         mbar_init(&sp_free, kPWarps);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&p_ready[b], kPWarps);
             mbar_init(&p_free[b], 1);
+            mbar_init(&w_go[b], kWWarps);
+            mbar_init(&w_free[b], 1);
+            mbar_init(&z_free[b], kSWarps);
+            mbar_init(&z_full[b], 1);
         }
-        mbar_init(&z_go, kVWarps + kSWarps);    // W is in place, and Z of the chunk before has been read
-        mbar_init(&z_full, 1);
-        mbar_init(&o_go, kVWarps + kSWarps);    // Sb is in place, and O1, O2 of the chunk before have been read
+        mbar_init(&o_go, kOWarps + kSWarps);   // Sb is in place, and O1, O2 of the chunk before have been read
         mbar_init(&sb_free, 1);
         mbar_init(&o_full, 1);
         mbar_init(&done, 1);
@@ -302,20 +307,32 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 const uint32_t q = base + s * F::STAGE, k = q + F::QB, v = k + F::KB;
                 const int s1 = s + 1 == NST ? 0 : s + 1, ph1 = s + 1 == NST ? ph ^ 1 : ph;
                 if (BOUNDARY && !(ok = bar_wait(&full[s], ph))) break;
-                if (!(ok = bar_wait(&z_go, c & 1))) break;
-                tc_fence_after();
+                // Z in two halves of the chunk's tokens, so that the warps of W fill one half while the other is used
                 const uint64_t kd = sdesc_mn_sw128(k, F::HALF);
+                const uint32_t zcol = tmu + F::Z + (c % F::NZ) * 128;
+                auto z_half = [&](int half) {
+                    tc_fence_after();
 #pragma unroll 1
-                for (int i = 0; i < 16; ++i)   // part i / 4, tokens 16 (i % 4) ..; the odd parts are negated
-                    mma_ts(tmu + F::Z, tmu + F::W + 8 * i, kd + (i & 3) * (2048 >> 4), id_z | ((i & 4) ? neg_a : 0u),
-                                i > 0);
-                mma_commit(&z_full);
-                if (!BOUNDARY) {
-                    if (c + 1 < nch) {
-                        if (!(ok = bar_wait(&full[s1], ph1) && bar_wait(&sp_free, c & 1))) break;
-                        tc_fence_after();
-                        scores(s1);
+                    for (int i = 0; i < 8; ++i) {   // part i / 2, tokens 32 half + 16 (i % 2) ..; the odd parts are negated
+                        const int sl = 2 * half + (i & 1);
+                        mma_ts(zcol, tmu + F::W + 32 * (i >> 1) + 8 * sl, kd + sl * (2048 >> 4), id_z | ((i & 2) ? neg_a : 0u),
+                               half + i > 0);
                     }
+                    mma_commit(&w_free[half]);
+                };
+                if (!(ok = bar_wait(&w_go[0], c & 1) &&
+                           (c < F::NZ || bar_wait(&z_free[c % F::NZ], (c / F::NZ - 1) & 1))))
+                    break;
+                z_half(0);
+                if (!BOUNDARY && c + 1 < nch) {
+                    if (!(ok = bar_wait(&full[s1], ph1) && bar_wait(&sp_free, c & 1))) break;
+                    tc_fence_after();
+                    scores(s1);
+                }
+                if (!(ok = bar_wait(&w_go[1], c & 1))) break;
+                z_half(1);
+                mma_commit(&z_full[c & 1]);
+                if (!BOUNDARY) {
                     if (!(ok = bar_wait(&o_go, c & 1))) break;
                     tc_fence_after();
                     const uint64_t qd = sdesc_k_sw128(q);
@@ -414,11 +431,9 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             }
         }
     } else if (w < 12) {
-        // ---------------- W and o: thread = channel of v, and one half of the chunk's tokens
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-        const int q4 = w & 3, ch = 32 * q4 + lane, tv = t - 128, half = (w - 4) / 4 * (C / 2);
-        constexpr int NV = 32 * kVWarps;
-        const bool mine = ch < DV;
+        const int q4 = w & 3, tg = t & 127;   // channels of v 32 q4 .. 32 q4 + 31, thread of the group
+        const bool mine = 32 * q4 < DV;
         const uint32_t lanes = static_cast<uint32_t>(32 * q4) << 16;
         // Of a 16-token x 16-channel tile (tokens t0.., channels 32 q4 + 16 lh ..) as four 8 x 8 matrices, channels
         // first: the row that this lane addresses, in a swizzled 64-channel half tile.
@@ -428,125 +443,150 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         };
         // A wait that runs out ends this warp's work, but not its part in the four warps' own barrier.
         auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && bar_wait(bar, parity); };
-        auto split = [&](int c) {
-            const int s = c % NST;
-            wait(&full[s], (c / NST) & 1);
-            uint8_t* kt = sm + s * F::STAGE + F::QB;
-            uint8_t* vt = kt + F::KB;
-            const int n = it.n - c * C;
-            if (n < C) {
-                // rows behind the sequence belong to others: they must not reach a sum, not even times zero
+        int s = 0, ph = 0;
+        if (w < 8) {
+            // ---------------- W
 #pragma unroll 1
-                for (int i = tv; ok && i < (C - n) * 8; i += NV) {
-                    const int r = n + i / 8, x = r * 128 + (i & 7) * 16;
+            for (int c = 0; c < nch; ++c) {
+                wait(&full[s], ph);
+                uint8_t* kt = sm + s * F::STAGE + F::QB;
+                uint8_t* vt = kt + F::KB;
+                const int n = it.n - c * C;
+                if (n < C) {
+                    // rows behind the sequence belong to others: they must not reach a sum, not even times zero
+#pragma unroll 1
+                    for (int i = tg; ok && i < (C - n) * 8; i += 128) {
+                        const int r = n + i / 8, x = r * 128 + (i & 7) * 16;
 #pragma unroll
-                    for (int b = 0; b < DK / 64; ++b) *reinterpret_cast<uint4*>(kt + b * F::HALF + x) = make_uint4(0u, 0u, 0u, 0u);
+                        for (int b = 0; b < DK / 64; ++b)
+                            *reinterpret_cast<uint4*>(kt + b * F::HALF + x) = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                    for (int b = 0; b < DV / 64; ++b) *reinterpret_cast<uint4*>(vt + b * F::HALF + x) = make_uint4(0u, 0u, 0u, 0u);
+                        for (int b = 0; b < DV / 64; ++b)
+                            *reinterpret_cast<uint4*>(vt + b * F::HALF + x) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    named_bar_sync(1, 128);
                 }
-                fence_proxy_async_smem();
-                named_bar_sync(1, NV);
-            }
-            if (c > 0) wait(&z_full, (c - 1) & 1);   // W of the chunk before has been read
-            if (mine && ok) {
-                tc_fence_after();
                 const Decays& d = decays[s];
-                uint4 wt[4];   // of this thread's token pair in each block of eight: w1, w2, -w3
-#pragma unroll
-                for (int b = 0; b < 4; ++b) wt[b] = d.w[half / 2 + 4 * b + (lane & 3)];
-#pragma unroll 1
-                for (int lh = 0; lh < 2; ++lh) {
-                    uint32_t v[2][4], u[4][8];
+                uint32_t v[2][4];
+                uint4 wb[4];   // w1, w2, -w3 of this thread's pair of tokens in each block of eight
+                auto load_v = [&](int lh, int half) {
                     ldsm_x4_trans(smem_u32(vt) + tile_row(half, lh), v[0]);
                     ldsm_x4_trans(smem_u32(vt) + tile_row(half + 16, lh), v[1]);
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) {   // block r / 2, channels 8 (r % 2) + lane / 4 of the sixteen
-                        const uint32_t x = v[r >> 2][r & 3];
-                        const uint4 wb = wt[r >> 1];
-                        u[0][r] = fma_bf16x2(x, wb.x, 0x80008000u);
-                        u[1][r] = fma_bf16x2(x, wb.x ^ 0x80008000u, u[0][r]);
-                        u[2][r] = fma_bf16x2(x, wb.y, 0x80008000u);
-                        u[3][r] = fma_bf16x2(x, wb.z, fma_bf16x2(x, wb.y ^ 0x80008000u, u[2][r]));
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tmem_st_16x128b_x4(tm + lanes + (static_cast<uint32_t>(16 * lh) << 16) + F::W + 32 * k + half / 2, u[k]);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-            }
-            __syncwarp();
-            if (lane == 0 && ok) {
-                mbar_arrive(&z_go);
-                if (BOUNDARY) mbar_arrive(&empty[s]);
-            }
-        };
-        auto out = [&](int c) {
-            const int s = c % NST, n = it.n - c * C;
-            wait(&o_full, c & 1);
-            uint8_t* ob = sm + F::O0 + (c & 1) * F::VB;
-            // the store that read this buffer two chunks ago is done with it
-            if (tv == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-            named_bar_sync(1, NV);
-            if (mine && ok) {
-                tc_fence_after();
-                const Decays& d = decays[s];
-                float2 e[4];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) e[b] = *reinterpret_cast<const float2*>(&d.eg[half + 8 * b + 2 * (lane & 3)]);
+                };
+                if (mine) load_v(0, 0);
 #pragma unroll 1
-                for (int lh = 0; lh < 2; ++lh) {
-                    float x[16], y[16];
-                    const uint32_t at = tm + lanes + (static_cast<uint32_t>(16 * lh) << 16) + half;
-                    tmem_ld_16x256b_x4(at + F::O1, x);
-                    tmem_ld_16x256b_x4(at + F::O2, y);
-                    tmem_wait_ld_regs<16>(x);
-                    tmem_wait_ld_regs<16>(y);
+                for (int half = 0; half < C; half += 32) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t u[4];
+                    for (int b = 0; b < 4; ++b) wb[b] = d.w[half / 2 + 4 * b + (lane & 3)];
+#pragma unroll 1
+                    for (int lh = 0; lh < 2; ++lh) {   // 16 channels, 32 tokens
+                        uint32_t u[4][8];
+                        if (mine) {
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {   // block 2 i + r / 2, channels 8 (r % 2) + lane / 4
-                            const int k = 8 * i + 2 * r;
-                            const float2 eb = e[2 * i + (r >> 1)];
-                            u[r] = pack_bf16x2(fmaf(eb.x, x[k], y[k]), fmaf(eb.y, x[k + 1], y[k + 1]));
+                            for (int r = 0; r < 8; ++r) {   // block r / 2, channels 8 (r % 2) + lane / 4 of the sixteen
+                                const uint32_t x = v[r >> 2][r & 3];
+                                const uint4 w4 = wb[r >> 1];
+                                u[0][r] = fma_bf16x2(x, w4.x, 0x80008000u);
+                                u[1][r] = fma_bf16x2(x, w4.x ^ 0x80008000u, u[0][r]);
+                                u[2][r] = fma_bf16x2(x, w4.y, 0x80008000u);
+                                u[3][r] = fma_bf16x2(x, w4.z, fma_bf16x2(x, w4.y ^ 0x80008000u, u[2][r]));
+                            }
+                            if (lh == 0) load_v(1, half);
+                            else if (half == 0) load_v(0, 32);
                         }
-                        stsm_x4_trans(smem_u32(ob) + tile_row(half + 16 * i, lh), u);
+                        if (lh == 0 && c > 0) wait(&w_free[half >> 5], (c - 1) & 1);
+                        if (mine && ok) {
+                            tc_fence_after();
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tmem_st_16x128b_x4(tm + lanes + (static_cast<uint32_t>(16 * lh) << 16) + F::W + 32 * k + half / 2,
+                                                   u[k]);
+                        }
+                    }
+                    if (mine && ok) tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0 && ok) mbar_arrive(&w_go[half >> 5]);
+                }
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(&empty[s]);
+                if (++s == NST) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+        } else if (!BOUNDARY) {
+            // ---------------- o
+            if (lane == 0) mbar_arrive(&o_go);   // there is no o before the first
+#pragma unroll 1
+            for (int c = 0; c < nch; ++c) {
+                const int n = it.n - c * C;
+                wait(&full[s], ph);
+                wait(&o_full, c & 1);
+                uint8_t* ob = sm + F::O0 + (c & 1) * F::VB;
+                // the store that read this buffer two chunks ago is done with it
+                if (tg == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                named_bar_sync(2, 128);
+                if (mine && ok) {
+                    tc_fence_after();
+                    const Decays& d = decays[s];
+#pragma unroll 1
+                    for (int u4 = 0; u4 < 4; ++u4) {   // 16 channels, 32 tokens
+                        const int lh = u4 & 1, half = (u4 >> 1) * 32;
+                        float x[16], y[16];
+                        const uint32_t at = tm + lanes + (static_cast<uint32_t>(16 * lh) << 16) + half;
+                        tmem_ld_16x256b_x4(at + F::O1, x);
+                        tmem_ld_16x256b_x4(at + F::O2, y);
+                        float2 e[4];
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) e[b] = *reinterpret_cast<const float2*>(&d.eg[half + 8 * b + 2 * (lane & 3)]);
+                        tmem_wait_ld_regs<16>(x);
+                        tmem_wait_ld_regs<16>(y);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t u[4];
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {   // block 2 i + r / 2, channels 8 (r % 2) + lane / 4
+                                const int k = 8 * i + 2 * r;
+                                const float2 eb = e[2 * i + (r >> 1)];
+                                u[r] = pack_bf16x2(fmaf(eb.x, x[k], y[k]), fmaf(eb.y, x[k + 1], y[k + 1]));
+                            }
+                            stsm_x4_trans(smem_u32(ob) + tile_row(half + 16 * i, lh), u);
+                        }
+                    }
+                    tc_fence_before();
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && ok) {
+                    mbar_arrive(&o_go);
+                    mbar_arrive(&empty[s]);
+                }
+                named_bar_sync(2, 128);
+                if (n >= C) {
+                    if (tg == 0 && ok) {
+#pragma unroll
+                        for (int b = 0; b < DV / 64; ++b) tma_store_2d(&mo, h * DV + 64 * b, it.t0 + c * C, ob + b * F::HALF);
+                        bulk_commit();
+                    }
+                } else {   // the rows behind the sequence are not this one's to write
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) +
+                                         (static_cast<size_t>(it.t0) + c * C) * a.H * DV + static_cast<size_t>(h) * DV;
+#pragma unroll 1
+                    for (int i = tg; ok && i < n * (DV / 8); i += 128) {
+                        const int r = i / (DV / 8), k8 = i % (DV / 8);
+                        st_global_v4(dst + static_cast<size_t>(r) * a.H * DV + 8 * k8,
+                                     *reinterpret_cast<const uint4*>(ob + (k8 >> 3) * F::HALF + r * 128 + (((k8 & 7) ^ (r & 7)) << 4)));
                     }
                 }
-                tc_fence_before();
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && ok) {
-                mbar_arrive(&o_go);
-                mbar_arrive(&empty[s]);
-            }
-            named_bar_sync(1, NV);
-            if (n >= C) {
-                if (tv == 0 && ok) {
-#pragma unroll
-                    for (int b = 0; b < DV / 64; ++b) tma_store_2d(&mo, h * DV + 64 * b, it.t0 + c * C, ob + b * F::HALF);
-                    bulk_commit();
-                }
-            } else {   // the rows behind the sequence are not this one's to write
-                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) +
-                                     (static_cast<size_t>(it.t0) + c * C) * a.H * DV + static_cast<size_t>(h) * DV;
-#pragma unroll 1
-                for (int i = tv; ok && i < n * (DV / 8); i += NV) {
-                    const int r = i / (DV / 8), k8 = i % (DV / 8);
-                    st_global_v4(dst + static_cast<size_t>(r) * a.H * DV + 8 * k8,
-                                 *reinterpret_cast<const uint4*>(ob + (k8 >> 3) * F::HALF + r * 128 + (((k8 & 7) ^ (r & 7)) << 4)));
+                if (++s == NST) {
+                    s = 0;
+                    ph ^= 1;
                 }
             }
-        };
-        if (lane == 0) mbar_arrive(&o_go);   // there is no o before the first
-#pragma unroll 1
-        for (int c = 0; c <= nch; ++c) {
-            if (c < nch) split(c);
-            if (!BOUNDARY && c > 0) out(c - 1);
+            if (tg == 0) bulk_wait0();
         }
-        if (!BOUNDARY && tv == 0) bulk_wait0();
     } else {
         // ---------------- state: thread = channel of v, S[i] = channel i of k
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsState));
@@ -562,7 +602,6 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         }
 #pragma unroll
         for (int i = 0; i < DK; ++i) S[i] = start && mine ? start[i * DV + ch] : 0.f;
-        if (lane == 0) mbar_arrive(&z_go);   // there is no Z before the first
         auto publish = [&]() {   // the bf16 copy that O1 multiplies q with
             if (mine) {
 #pragma unroll
@@ -603,13 +642,13 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             const float eC = decays[s].eC;
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
-            if (!(ok = bar_wait(&z_full, c & 1))) break;
+            if (!(ok = bar_wait(&z_full[c & 1], (c >> 1) & 1))) break;
             if (mine) {
                 tc_fence_after();
 #pragma unroll
                 for (int b = 0; b < DK; b += 32) {
                     float z[32];
-                    tmem_ld32(tm + lanes + F::Z + b, z);
+                    tmem_ld32(tm + lanes + F::Z + (c % F::NZ) * 128 + b, z);
                     tmem_wait_ld_regs<32>(z);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) S[b + i] = fmaf(eC, S[b + i], z[i]);
@@ -617,7 +656,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 tc_fence_before();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&z_go);
+            if (lane == 0) mbar_arrive(&z_free[c % F::NZ]);
             // a checkpoint, and the state at the segment's end
             float* dst = nullptr;
             to_ck -= C;
