@@ -149,6 +149,11 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
     return false;
 }
 
+// 4 bytes global -> shared by an asynchronous copy, zero when not `valid` (nothing is read then)
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+
 // e^x for x <= 0 to about one unit in the last place: 2^(x log2 e) with the rounding of the product put back.
 __device__ __forceinline__ float exp_fast(float x) {
     const float y = x * kLog2e, r = fmaf(x, kLog2e, -y) + x * 1.9259629e-8f;   // log2(e) - kLog2e
@@ -165,6 +170,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ Decays decays[NST];
+    __shared__ __align__(8) float la_ring[4][C];
     __shared__ __align__(8) uint64_t full[NST], empty[NST], sp_full, sp_free, p_ready[2], p_free[2], w_go[2], w_free[2], z_free[2],
         z_full[2], o_go, sb_free, o_full, done;
     __shared__ uint32_t tmem_slot;
@@ -212,17 +218,23 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (w == 2) {
             // ---------------- producer
-            // this lane's tokens 2 lane and 2 lane + 1 of the chunk
+            // log_alpha of this lane's tokens 2 lane and 2 lane + 1, three chunks ahead: a load takes longer than a
+            // chunk.  Copied to shared memory, since moving a value on in registers would wait for its load.
             const float* la = a.la + (static_cast<size_t>(it.t0) + 2 * lane) * a.la_t + h;
+            const uint32_t la_at = smem_u32(&la_ring[0][2 * lane]);
             int left = it.n - 2 * lane;   // tokens of the segment from the lane's first one on
-            auto log_alpha = [&](float& x0, float& x1) {
-                x0 = left > 0 ? fmaxf(la[0], kLinLogMin) : 0.f;
-                x1 = left > 1 ? fmaxf(la[a.la_t], kLinLogMin) : 0.f;
+            auto fetch = [&](int c) {
+                const uint32_t at = la_at + (c & 3) * static_cast<uint32_t>(sizeof(la_ring[0]));
+                cp_async4(at, left > 0 ? la : a.la, left > 0);
+                cp_async4(at + 4, left > 1 ? la + a.la_t : a.la, left > 1);
+                asm volatile("cp.async.commit_group;" ::: "memory");
                 la += C * static_cast<size_t>(a.la_t);
                 left -= C;
             };
-            float x0, x1, total = 0.f;
-            log_alpha(x0, x1);
+            float total = 0.f;
+            if (nch > 0)
+#pragma unroll 1
+                for (int c = 0; c < 3; ++c) fetch(c);
             int s = 0, ph = 1, issued = 0;
 #pragma unroll 1
             for (int c = 0; c < nch; ++c) {
@@ -241,6 +253,11 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         tma_load_2d(sb + F::QB + F::KB + b * F::HALF, &mv, h * DV + 64 * b, tok, &full[s]);
                 }
                 issued = c + 1;
+                fetch(c + 3);
+                asm volatile("cp.async.wait_group 3;" ::: "memory");
+                const float2 x = *reinterpret_cast<const float2*>(&la_ring[c & 3][2 * lane]);
+                const bool in0 = c * C + 2 * lane < it.n, in1 = c * C + 2 * lane + 1 < it.n;
+                const float x0 = in0 ? fmaxf(x.x, kLinLogMin) : 0.f, x1 = in1 ? fmaxf(x.y, kLinLogMin) : 0.f;
                 // inclusive sums of the lanes' pairs, from the chunk's start and from its end
                 float f = x0 + x1, r = f;
 #pragma unroll 1
@@ -276,13 +293,13 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 total += sum;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[s]);
-                log_alpha(x0, x1);   // of the next chunk
                 if (++s == NST) {
                     s = 0;
                     ph ^= 1;
                 }
             }
             if (BOUNDARY && lane == 0) a.zdecay[static_cast<size_t>(it.z0 + it.seg) * a.H + h] = exp_fast(total);
+            cp_async_wait_all();
             // no copy stays in flight behind the CTA: wait (bounded, quietly) for the last fill of every stage
     #pragma unroll 1
         for (int c = issued > NST ? issued - NST : 0; c < issued; ++c) bar_wait(&full[c % NST], (c / NST) & 1);
