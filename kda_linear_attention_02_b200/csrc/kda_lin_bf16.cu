@@ -45,6 +45,9 @@ struct Cfg {
     static constexpr uint32_t QB = BOUNDARY ? 0 : DK / 64 * HALF, KB = DK / 64 * HALF, VB = DV / 64 * HALF;
     static constexpr uint32_t STAGE = QB + KB + VB;
     static constexpr int NST = BOUNDARY ? 5 : (STAGE > 40960 ? 3 : 4);
+    // Decays outlive their chunk's tiles: the last to read those of chunk c, in writing o (the boundary pass: in
+    // taking Z), is done before the products of chunk c + 2 are, and those free the tiles of chunk c + 2 + NST.
+    static constexpr int ND = NST + 2;
     static constexpr uint32_t PB = C * 128;                          // P: 64 rows of 64 bf16
     static constexpr uint32_t P0 = NST * STAGE, O0 = P0 + (BOUNDARY ? 0 : 2 * PB);
     // the A operands of 128 rows read past 64-row tiles (their results are not used): the tiles behind exist
@@ -169,7 +172,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
     constexpr int NST = F::NST, C = F::C;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    __shared__ Decays decays[NST];
+    __shared__ Decays decays[F::ND];
     __shared__ __align__(8) float la_ring[4][C];
     __shared__ __align__(8) uint64_t full[NST], empty[NST], sp_full, sp_free, p_ready[2], p_free[2], w_go[2], w_free[2], z_free[2],
         z_full[2], o_go, sb_free, o_full, done;
@@ -178,7 +181,9 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
     if (t == 0) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(&full[s], 2);
-            mbar_init(&empty[s], 1 + kWWarps + kSWarps + (BOUNDARY ? 0 : kPWarps + kOWarps));
+            // the chunk's last product is done, and with it all that read its tiles (in the boundary pass nothing of a
+            // chunk waits for the state warps, which therefore say themselves that they have seen the filling)
+            mbar_init(&empty[s], 1 + (BOUNDARY ? kSWarps : 0));
         }
         mbar_init(&sp_full, 1);
         mbar_init(&sp_free, kPWarps);
@@ -270,7 +275,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 if (lane == 0) before = 0.f;
                 if (lane == 31) after = 0.f;
                 const float sum = __shfl_sync(0xffffffffu, f, 31), gm = __shfl_sync(0xffffffffu, f, 15);
-                Decays& d = decays[s];
+                Decays& d = decays[c % F::ND];
                 const float2 g = make_float2(before + x0, f);
                 *reinterpret_cast<float2*>(&d.g2[2 * lane]) = make_float2(g.x * kLog2e, g.y * kLog2e);
                 *reinterpret_cast<float2*>(&d.eg[2 * lane]) = make_float2(exp_fast(g.x), exp_fast(g.y));
@@ -392,7 +397,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 for (int c = 0; c < nch; ++c) {
                     if (!(ok = bar_wait(&full[s], ph) && bar_wait(&sp_full, c & 1))) break;
                     tc_fence_after();
-                    const Decays& d = decays[s];
+                    const Decays& d = decays[c % F::ND];
                     const float gr = d.g2[row];
                     const uint32_t at = tm + F::SP + (static_cast<uint32_t>(32 * w) << 16);
                     if (c >= 2 && !(ok = bar_wait(&p_free[c & 1], ((c >> 1) - 1) & 1))) break;
@@ -433,10 +438,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&sp_free);
-                        mbar_arrive(&empty[s]);
-                    }
+                    if (lane == 0) mbar_arrive(&sp_free);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&p_ready[c & 1]);
@@ -484,7 +486,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     fence_proxy_async_smem();
                     named_bar_sync(1, 128);
                 }
-                const Decays& d = decays[s];
+                const Decays& d = decays[c % F::ND];
                 uint32_t v[2][4];
                 uint4 wb[4];   // w1, w2, -w3 of this thread's pair of tokens in each block of eight
                 auto load_v = [&](int lh, int half) {
@@ -526,8 +528,6 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     __syncwarp();
                     if (lane == 0 && ok) mbar_arrive(&w_go[half >> 5]);
                 }
-                __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(&empty[s]);
                 if (++s == NST) {
                     s = 0;
                     ph ^= 1;
@@ -535,11 +535,21 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             }
         } else if (!BOUNDARY) {
             // ---------------- o
-            if (lane == 0) mbar_arrive(&o_go);   // there is no o before the first
+            // Leave for o of chunk c is given with the chunk's decays in sight: a stage is filled anew as soon as its
+            // products are done, so nobody may look for a filling after it has let those go ahead.
+            auto leave = [&]() {
+                wait(&full[s], ph);
+                if (++s == NST) {
+                    s = 0;
+                    ph ^= 1;
+                }
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(&o_go);
+            };
+            if (nch > 0) leave();
 #pragma unroll 1
             for (int c = 0; c < nch; ++c) {
                 const int n = it.n - c * C;
-                wait(&full[s], ph);
                 wait(&o_full, c & 1);
                 uint8_t* ob = sm + F::O0 + (c & 1) * F::VB;
                 // the store that read this buffer two chunks ago is done with it
@@ -547,7 +557,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 named_bar_sync(2, 128);
                 if (mine && ok) {
                     tc_fence_after();
-                    const Decays& d = decays[s];
+                    const Decays& d = decays[c % F::ND];
 #pragma unroll 1
                     for (int u4 = 0; u4 < 4; ++u4) {   // 16 channels, 32 tokens
                         const int lh = u4 & 1, half = (u4 >> 1) * 32;
@@ -575,11 +585,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     tc_fence_before();
                 }
                 fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0 && ok) {
-                    mbar_arrive(&o_go);
-                    mbar_arrive(&empty[s]);
-                }
+                if (c + 1 < nch) leave();
                 named_bar_sync(2, 128);
                 if (n >= C) {
                     if (tg == 0 && ok) {
@@ -596,10 +602,6 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         st_global_v4(dst + static_cast<size_t>(r) * a.H * DV + 8 * k8,
                                      *reinterpret_cast<const uint4*>(ob + (k8 >> 3) * F::HALF + r * 128 + (((k8 & 7) ^ (r & 7)) << 4)));
                     }
-                }
-                if (++s == NST) {
-                    s = 0;
-                    ph ^= 1;
                 }
             }
             if (tg == 0) bulk_wait0();
@@ -650,15 +652,16 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         int s = 0, ph = 0;
 #pragma unroll 1
         for (int c = 0; c < nch; ++c) {
-            if (!BOUNDARY) {
+            if (!(ok = bar_wait(&full[s], ph))) break;   // before Sb lets the chunk's products go ahead (see `leave`)
+            const float eC = decays[c % F::ND].eC;
+            if (BOUNDARY) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[s]);
+            } else {
                 if (c > 0 && !(ok = bar_wait(&sb_free, (c - 1) & 1))) break;   // the copy of the chunk before has been read
                 tc_fence_after();
                 publish();
             }
-            if (!(ok = bar_wait(&full[s], ph))) break;
-            const float eC = decays[s].eC;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
             if (!(ok = bar_wait(&z_full[c & 1], (c >> 1) & 1))) break;
             if (mine) {
                 tc_fence_after();
