@@ -392,6 +392,9 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         *reinterpret_cast<uint4*>(p + (((j0 / 8 + i) ^ (row & 7)) << 4)) =
                             make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
                 };
+                uint32_t mask[16];   // of the diagonal block's pairs: columns up to the row's own
+#pragma unroll
+                for (int j = 0; j < 16; ++j) mask[j] = 2 * j + 1 <= lane ? 0xffffffffu : 2 * j <= lane ? 0x0000ffffu : 0u;
                 int s = 0, ph = 0;
 #pragma unroll 1
                 for (int c = 0; c < nch; ++c) {
@@ -419,23 +422,21 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         }
                         put(p, j0, u);
                     }
-#pragma unroll 1
-                    for (int j0 = 32 * w; j0 < 32 * w + 32; j0 += 16) {
-                        float x[16];
-                        uint32_t u[8];
-                        tmem_ld16(at + j0, x);
-                        tmem_wait_ld_regs<16>(x);
-                        const int k = row - j0;   // the row's own column
+                    float x[32];
+                    uint32_t u[16];
+                    tmem_ld32(at + 32 * w, x);
+                    tmem_wait_ld_regs<32>(x);
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 g = *reinterpret_cast<const float4*>(&d.g2[j0 + j]);
-                            u[j / 2] = pack_bf16x2(j <= k ? x[j] * ex2_approx(gr - g.x) : 0.f,
-                                                   j + 1 <= k ? x[j + 1] * ex2_approx(gr - g.y) : 0.f);
-                            u[j / 2 + 1] = pack_bf16x2(j + 2 <= k ? x[j + 2] * ex2_approx(gr - g.z) : 0.f,
-                                                       j + 3 <= k ? x[j + 3] * ex2_approx(gr - g.w) : 0.f);
-                        }
-                        put(p, j0, u);
+                    for (int j = 0; j < 32; j += 4) {   // what lies above the diagonal is cut off after the packing
+                        const float4 g = *reinterpret_cast<const float4*>(&d.g2[32 * w + j]);
+                        u[j / 2] = mask[j / 2] & pack_bf16x2(x[j] * ex2_approx(gr - g.x), x[j + 1] * ex2_approx(gr - g.y));
+                        u[j / 2 + 1] =
+                            mask[j / 2 + 1] & pack_bf16x2(x[j + 2] * ex2_approx(gr - g.z), x[j + 3] * ex2_approx(gr - g.w));
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4*>(p + (((4 * w + i) ^ (row & 7)) << 4)) =
+                            make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sp_free);
@@ -454,12 +455,14 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         const int q4 = w & 3, tg = t & 127;   // channels of v 32 q4 .. 32 q4 + 31, thread of the group
         const bool mine = 32 * q4 < DV;
         const uint32_t lanes = static_cast<uint32_t>(32 * q4) << 16;
-        // Of a 16-token x 16-channel tile (tokens t0.., channels 32 q4 + 16 lh ..) as four 8 x 8 matrices, channels
-        // first: the row that this lane addresses, in a swizzled 64-channel half tile.
-        auto tile_row = [&](int t0, int lh) {
-            const int tok = t0 + ((lane >> 4) << 3) + (lane & 7), c8 = 32 * q4 + 16 * lh + (lane & 8);
+        // Of a 16-token x 16-channel tile (channels 32 q4 + 16 lh ..) as four 8 x 8 matrices, channels first: the row
+        // that this lane addresses in a swizzled 64-channel half tile, for the chunk's first tokens (128 bytes on for
+        // each further token; the swizzle repeats every eight).
+        auto tile_row = [&](int lh) {
+            const int tok = ((lane >> 4) << 3) + (lane & 7), c8 = 32 * q4 + 16 * lh + (lane & 8);
             return (c8 >> 6) * F::HALF + tok * 128 + ((((c8 & 63) >> 3) ^ (tok & 7)) << 4);
         };
+        const uint32_t row0 = tile_row(0), row1 = tile_row(1);
         // A wait that runs out ends this warp's work, but not its part in the four warps' own barrier.
         auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && bar_wait(bar, parity); };
         int s = 0, ph = 0;
@@ -489,11 +492,11 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 const Decays& d = decays[c % F::ND];
                 uint32_t v[2][4];
                 uint4 wb[4];   // w1, w2, -w3 of this thread's pair of tokens in each block of eight
-                auto load_v = [&](int lh, int half) {
-                    ldsm_x4_trans(smem_u32(vt) + tile_row(half, lh), v[0]);
-                    ldsm_x4_trans(smem_u32(vt) + tile_row(half + 16, lh), v[1]);
+                auto load_v = [&](uint32_t row, int half) {
+                    ldsm_x4_trans(smem_u32(vt) + row + half * 128, v[0]);
+                    ldsm_x4_trans(smem_u32(vt) + row + half * 128 + 16 * 128, v[1]);
                 };
-                if (mine) load_v(0, 0);
+                if (mine) load_v(row0, 0);
 #pragma unroll 1
                 for (int half = 0; half < C; half += 32) {
 #pragma unroll
@@ -511,8 +514,8 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                                 u[2][r] = fma_bf16x2(x, w4.y, 0x80008000u);
                                 u[3][r] = fma_bf16x2(x, w4.z, fma_bf16x2(x, w4.y ^ 0x80008000u, u[2][r]));
                             }
-                            if (lh == 0) load_v(1, half);
-                            else if (half == 0) load_v(0, 32);
+                            if (lh == 0) load_v(row1, half);
+                            else if (half == 0) load_v(row0, 32);
                         }
                         if (lh == 0 && c > 0) wait(&w_free[half >> 5], (c - 1) & 1);
                         if (mine && ok) {
@@ -579,7 +582,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                                 const float2 eb = e[2 * i + (r >> 1)];
                                 u[r] = pack_bf16x2(fmaf(eb.x, x[k], y[k]), fmaf(eb.y, x[k + 1], y[k + 1]));
                             }
-                            stsm_x4_trans(smem_u32(ob) + tile_row(half + 16 * i, lh), u);
+                            stsm_x4_trans(smem_u32(ob) + (lh ? row1 : row0) + (half + 16 * i) * 128, u);
                         }
                     }
                     tc_fence_before();
