@@ -321,8 +321,8 @@ KDA_API kda_status_t kda_lin_recurrent_step(float* state, int64_t n_states, cons
  *   table  [n_rows, max_pages]  the pages of each row, in order; entries behind a row's count mean nothing
  *   counts [n_rows]             pages of each row
  *
- * kda_pages_fork: opens n rows.  Row children[i] continues row parents[i]: its first n_shared[i] pages are
- *   the parent's own (refs + 1), the parent's other pages are copied to new pages, and n_fresh[i] further
+ * kda_pages_fork: opens n rows.  Row children[i] continues row parents[i]: its first n_shared[i] pages (NULL:
+ *   none) are the parent's own (refs + 1), the parent's other pages are copied to new pages, and n_fresh[i] further
  *   new pages (n_fresh NULL: none) follow, zeroed when zero_fresh is set and otherwise as they were.
  *   parents[i] = -1 opens a row of fresh pages alone; parents[i] = children[i] appends the fresh pages to
  *   that row.  New pages are the free ones in ascending order, given out in order of i and of the page's

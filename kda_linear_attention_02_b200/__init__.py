@@ -342,27 +342,57 @@ def kda_lin_chunk_fwd_workspace_bytes(total_tokens, n_seqs, H, dk, dv, dtype=KDA
                                                          int(dtype)))
 
 
-def _launch_on(t: torch.Tensor, name: str, stream):
-    """(device guard, stream) of a call whose tensors live where `t` does: the given stream, else the current
-    one of that device, which the guard makes the current device for the launch."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if stream is not None and stream.device != t.device:
-        raise ValueError(f"stream: expected device {t.device}, got {stream.device}")
-    return torch.cuda.device(t.device), torch.cuda.current_stream(t.device) if stream is None else stream
+class _Launch:
+    """Where a call runs: the stream (the given one, else the current one of the tensors' device) as a raw pointer
+    in `.raw`, with that device current inside the with block.  The checks and the switch of device cost nothing
+    when the device is current already, which is what keeps the small calls short."""
+
+    __slots__ = ("raw", "stream", "dev", "back")
+
+    def __init__(self, t: torch.Tensor, name: str, stream):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on a CUDA device")
+        self.dev, self.stream, self.back = t.device, stream, None
+        if stream is None:
+            self.raw = torch._C._cuda_getCurrentRawStream(self.dev.index)
+        else:
+            if stream.device != self.dev:
+                raise ValueError(f"stream: expected device {self.dev}, got {stream.device}")
+            self.raw = stream.cuda_stream
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        if cur != self.dev.index:
+            self.back = cur
+            torch.cuda.set_device(self.dev.index)
+        return self
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+    def empty(self, n, dtype=torch.uint8):
+        """A 1-D tensor that belongs to the call's stream: its memory is used again in that stream's order."""
+        if self.stream is None:
+            return torch.empty(n, dtype=dtype, device=self.dev)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(n, dtype=dtype, device=self.dev)
 
 
-def _scratch(nbytes, dev, stream):
-    """uint8 scratch from torch's allocator that belongs to the stream the kernels run on: its memory is reused
-    in that stream's order."""
-    with torch.cuda.stream(stream):
-        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
+def _same(t, name, shape, dtype, dev):
+    """_need for the hot calls: the checks first, the messages only when one fails."""
+    if t is None or t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        _need(t, name, shape, dtype, dev)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _log_alpha(log_alpha, n, H, dev):
     """Checks log_alpha and tells whether it is per token ([n, H]) or a constant of each head ([H])."""
     per_token = log_alpha is None or log_alpha.dim() != 1
-    _need(log_alpha, "log_alpha", (n, H) if per_token else (H,), torch.float32, dev)
+    _same(log_alpha, "log_alpha", (n, H) if per_token else (H,), torch.float32, dev)
     return int(per_token)
 
 
@@ -376,36 +406,42 @@ def kda_lin_chunk_fwd(q, k, v, log_alpha, initial_state, cu_seqlens, o, final_st
     checkpoints, ckpt_cu and workspace as in kda_chunk_fwd.  Outputs are written in place.
     """
     _need(q, "q")
-    dev = q.device
     if q.dim() != 3 or v is None or v.dim() != 3 or cu_seqlens is None:
         raise ValueError("q, v must be [T, heads, channels] and cu_seqlens [N + 1]")
+    dev, qt, f32 = q.device, q.dtype, torch.float32
     T, Hqk, dk = q.shape
-    H, dv = v.shape[1], v.shape[2]
+    _, H, dv = v.shape
     dt = _dtype_code(q)
     n = cu_seqlens.numel() - 1
-    _need(k, "k", (T, Hqk, dk), q.dtype, dev)
-    _need(v, "v", (T, H, dv), q.dtype, dev)
-    _need(o, "o", (T, H, dv), q.dtype, dev)
+    _same(k, "k", (T, Hqk, dk), qt, dev)
+    _same(v, "v", (T, H, dv), qt, dev)
+    _same(o, "o", (T, H, dv), qt, dev)
     per_token = _log_alpha(log_alpha, T, H, dev)
-    _need(cu_seqlens, "cu_seqlens", (n + 1,), torch.int32, dev)
-    _opt(initial_state, "initial_state", (n, H, dk, dv), torch.float32, dev)
-    _opt(final_state, "final_state", (n, H, dk, dv), torch.float32, dev)
+    _same(cu_seqlens, "cu_seqlens", (n + 1,), torch.int32, dev)
+    if initial_state is not None:
+        _same(initial_state, "initial_state", (n, H, dk, dv), f32, dev)
+    if final_state is not None:
+        _same(final_state, "final_state", (n, H, dk, dv), f32, dev)
+    ck = cc = None
     if ckpt_stride:
-        _need(checkpoints, "checkpoints", None, torch.float32, dev)
-        if checkpoints.dim() != 4 or tuple(checkpoints.shape[1:]) != (H, dk, dv):
+        _need(checkpoints, "checkpoints", None, f32, dev)
+        if checkpoints.dim() != 4 or checkpoints.shape[1:] != (H, dk, dv):
             raise ValueError("checkpoints must be [n_ckpt, H, dk, dv]")
-        _need(ckpt_cu, "ckpt_cu", (n + 1,), torch.int32, dev)
-    guard, stream = _launch_on(q, "q", stream)
-    if workspace is None:
-        workspace = _scratch(kda_lin_chunk_fwd_workspace_bytes(T, n, H, dk, dv, dt), dev, stream)
-    _need(workspace, "workspace", None, torch.uint8, dev)
-    ck = bool(ckpt_stride) and checkpoints.numel() > 0
-    with guard:
-        st = _load().kda_lin_chunk_fwd(_p(q), _p(k), _p(v), _p(log_alpha), per_token, _p(initial_state), _p(cu_seqlens),
-                                       n, T, Hqk, H, dk, dv, dt, int(ckpt_stride) if ck else 0, _p(o), _p(final_state),
-                                       _p(checkpoints if ck else None), _p(ckpt_cu if ck else None), _p(workspace),
-                                       workspace.numel(), ctypes.c_void_p(stream.cuda_stream))
-    _check(st, "kda_lin_chunk_fwd")
+        _same(ckpt_cu, "ckpt_cu", (n + 1,), torch.int32, dev)
+        if checkpoints.numel():
+            ck, cc = checkpoints.data_ptr(), ckpt_cu.data_ptr()
+    L = _load()
+    with _Launch(q, "q", stream) as on:
+        if workspace is None:
+            workspace = on.empty(max(L.kda_lin_chunk_fwd_workspace_bytes(T, n, H, dk, dv, dt), 256))
+        else:
+            _need(workspace, "workspace", None, torch.uint8, dev)
+        st = L.kda_lin_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), per_token,
+                                 _ptr(initial_state), cu_seqlens.data_ptr(), n, T, Hqk, H, dk, dv, dt,
+                                 int(ckpt_stride) if ck else 0, o.data_ptr(), _ptr(final_state), ck, cc,
+                                 workspace.data_ptr(), workspace.numel(), on.raw)
+    if st:
+        _check(st, "kda_lin_chunk_fwd")
     return o
 
 
@@ -417,32 +453,33 @@ def kda_lin_recurrent_step(state, q, k, v, log_alpha, o, *, slots=None, stream=N
     row; a negative slot marks an idle row, which is left alone.  None: row i uses state i.
     """
     _need(state, "state", None, torch.float32)
-    dev = state.device
     if state.dim() != 4 or q is None or q.dim() != 3:
         raise ValueError("state must be [n_states, H, dk, dv] and q [n, Hqk, dk]")
+    dev, qt = state.device, q.dtype
     n_states, H, dk, dv = state.shape
-    n, Hqk = q.shape[0], q.shape[1]
+    n, Hqk, _ = q.shape
     dt = _dtype_code(q)
-    _need(q, "q", (n, Hqk, dk), q.dtype, dev)
-    _need(k, "k", (n, Hqk, dk), q.dtype, dev)
-    _need(v, "v", (n, H, dv), q.dtype, dev)
-    _need(o, "o", (n, H, dv), q.dtype, dev)
+    _same(q, "q", (n, Hqk, dk), qt, dev)
+    _same(k, "k", (n, Hqk, dk), qt, dev)
+    _same(v, "v", (n, H, dv), qt, dev)
+    _same(o, "o", (n, H, dv), qt, dev)
     per_token = _log_alpha(log_alpha, n, H, dev)
     stride = 1
     if slots is not None:
-        if slots.dim() != 1 or slots.shape[0] != n or slots.dtype != torch.int32 or slots.device != dev:
+        if slots.shape != (n,) or slots.dtype != torch.int32 or slots.device != dev:
             raise ValueError(f"slots must be int32 [{n}] on {dev}")
-        stride = slots.stride(0) if n > 1 else 1
-        if stride <= 0:
-            raise ValueError("slots: entries must not share memory")
+        if n > 1:
+            stride = slots.stride(0)
+            if stride <= 0:
+                raise ValueError("slots: entries must not share memory")
     elif n > n_states:
         raise ValueError(f"{n} rows need as many states, got {n_states}")
-    guard, stream = _launch_on(state, "state", stream)
-    with guard:
-        st = _load().kda_lin_recurrent_step(_p(state), n_states, _p(slots), stride, _p(q), _p(k), _p(v), _p(log_alpha),
-                                            per_token, n, Hqk, H, dk, dv, dt, _p(o),
-                                            ctypes.c_void_p(stream.cuda_stream))
-    _check(st, "kda_lin_recurrent_step")
+    with _Launch(state, "state", stream) as on:
+        st = _load().kda_lin_recurrent_step(state.data_ptr(), n_states, _ptr(slots), stride, q.data_ptr(), k.data_ptr(),
+                                            v.data_ptr(), log_alpha.data_ptr(), per_token, n, Hqk, H, dk, dv, dt,
+                                            o.data_ptr(), on.raw)
+    if st:
+        _check(st, "kda_lin_recurrent_step")
     return o
 
 
@@ -450,9 +487,7 @@ def _page_bytes(t, name, first):
     _need(t, name)
     if t.dim() < first + 1 or t.numel() == 0:
         raise ValueError(f"{name} must be {'[n_planes, n_pages, ...]' if first == 2 else '[n_pages, ...]'} and not empty")
-    n = t.element_size()
-    for x in t.shape[first:]:
-        n *= x
+    n = t.numel() * t.element_size() // (t.shape[0] * t.shape[1] if first == 2 else t.shape[0])
     if n % 16:
         raise ValueError(f"{name}: a page has {n} bytes, not a multiple of 16")
     return n
@@ -466,25 +501,36 @@ def kda_pages_copy(dst, src, dst_pages=None, src_pages=None, *, stream=None):
     that copy out, and one source may go to many destinations.
     """
     nb = _page_bytes(dst, "dst", 1)
-    _need(src, "src", (src.shape[0], *dst.shape[1:]) if src is not None and src.dim() else None, dst.dtype, dst.device)
-    lens = [t.shape[0] for t in (dst_pages, src_pages) if t is not None and t.dim() == 1]
-    n = lens[0] if lens else src.shape[0]
-    _opt(dst_pages, "dst_pages", (n,), torch.int32, dst.device)
-    _opt(src_pages, "src_pages", (n,), torch.int32, dst.device)
-    guard, stream = _launch_on(dst, "dst", stream)
-    with guard:
-        st = _load().kda_pages_copy(_p(dst), dst.shape[0], _p(src), src.shape[0], _p(dst_pages), _p(src_pages), n, nb,
-                                    ctypes.c_void_p(stream.cuda_stream))
-    _check(st, "kda_pages_copy")
+    dev = dst.device
+    _need(src, "src", None, dst.dtype, dev)
+    if src.shape[1:] != dst.shape[1:]:
+        raise ValueError(f"src: expected pages of shape {tuple(dst.shape[1:])}, got {tuple(src.shape[1:])}")
+    n = src.shape[0]
+    for x in (src_pages, dst_pages):
+        if x is not None:
+            n = x.numel()
+    if dst_pages is not None:
+        _same(dst_pages, "dst_pages", (n,), torch.int32, dev)
+    if src_pages is not None:
+        _same(src_pages, "src_pages", (n,), torch.int32, dev)
+    with _Launch(dst, "dst", stream) as on:
+        st = _load().kda_pages_copy(dst.data_ptr(), dst.shape[0], src.data_ptr(), src.shape[0], _ptr(dst_pages),
+                                    _ptr(src_pages), n, nb, on.raw)
+    if st:
+        _check(st, "kda_pages_copy")
     return dst
 
 
 def _book(refs, table, counts, dev):
+    """Checks the bookkeeping of a batch; returns (n_pages, n_rows, max_pages)."""
     if refs is None or table is None or refs.dim() != 1 or table.dim() != 2:
         raise ValueError("refs must be [n_pages] and table [n_rows, max_pages]")
-    _need(refs, "refs", None, torch.int32, dev)
-    _need(table, "table", None, torch.int32, dev)
-    _need(counts, "counts", (table.shape[0],), torch.int32, dev)
+    i32 = torch.int32
+    _same(refs, "refs", refs.shape, i32, dev)
+    _same(table, "table", table.shape, i32, dev)
+    rows, most = table.shape
+    _same(counts, "counts", (rows,), i32, dev)
+    return refs.shape[0], rows, most
 
 
 def kda_pages_fork(pool, refs, table, counts, parents, children, n_shared=None, n_fresh=None, *, zero_fresh=False,
@@ -498,41 +544,43 @@ def kda_pages_fork(pool, refs, table, counts, parents, children, n_shared=None, 
     row is extended.  A call that cannot be carried out changes nothing; kda_get_device_status tells why.
     """
     nb = _page_bytes(pool, "pool", 2)
-    dev = pool.device
-    _book(refs, table, counts, dev)
-    if refs.shape[0] != pool.shape[1]:
-        raise ValueError(f"refs: expected {pool.shape[1]} pages, got {refs.shape[0]}")
-    _need(parents, "parents", None, torch.int32, dev)
+    dev, i32 = pool.device, torch.int32
+    n_pages, rows, most = _book(refs, table, counts, dev)
+    if n_pages != pool.shape[1]:
+        raise ValueError(f"refs: expected {pool.shape[1]} pages, got {n_pages}")
+    _need(parents, "parents", None, i32, dev)
     n = parents.numel()
-    guard, stream = _launch_on(pool, "pool", stream)
-    if n_shared is None:
-        with torch.cuda.stream(stream):
-            n_shared = torch.zeros(n, dtype=torch.int32, device=dev)
-    for x, name in ((parents, "parents"), (children, "children"), (n_shared, "n_shared")):
-        _need(x, name, (n,), torch.int32, dev)
-    _opt(n_fresh, "n_fresh", (n,), torch.int32, dev)
-    rows, most = table.shape
-    if workspace is None:
-        workspace = _scratch(_load().kda_pages_fork_workspace_bytes(n, most), dev, stream)
-    _need(workspace, "workspace", None, torch.uint8, dev)
-    with guard:
-        st = _load().kda_pages_fork(_p(pool), pool.shape[0], pool.shape[1], nb, _p(refs), _p(table), _p(counts), rows, most,
-                                    _p(parents), _p(children), _p(n_shared), _p(n_fresh), n, int(bool(zero_fresh)),
-                                    _p(workspace), workspace.numel(), ctypes.c_void_p(stream.cuda_stream))
-    _check(st, "kda_pages_fork")
+    _same(parents, "parents", (n,), i32, dev)
+    _same(children, "children", (n,), i32, dev)
+    if n_shared is not None:
+        _same(n_shared, "n_shared", (n,), i32, dev)
+    if n_fresh is not None:
+        _same(n_fresh, "n_fresh", (n,), i32, dev)
+    L = _load()
+    with _Launch(pool, "pool", stream) as on:
+        if workspace is None:
+            workspace = on.empty(max(L.kda_pages_fork_workspace_bytes(n, most), 256))
+        else:
+            _need(workspace, "workspace", None, torch.uint8, dev)
+        st = L.kda_pages_fork(pool.data_ptr(), pool.shape[0], n_pages, nb, refs.data_ptr(), table.data_ptr(),
+                              counts.data_ptr(), rows, most, parents.data_ptr(), children.data_ptr(), _ptr(n_shared),
+                              _ptr(n_fresh), n, 1 if zero_fresh else 0, workspace.data_ptr(), workspace.numel(), on.raw)
+    if st:
+        _check(st, "kda_pages_fork")
 
 
 def kda_pages_free(refs, table, counts, rows, *, stream=None):
     """Frees the rows: each of their pages loses a reference, their counts become 0 (C: kda_pages_free)."""
     _need(refs, "refs")
     dev = refs.device
-    _book(refs, table, counts, dev)
-    _need(rows, "rows", (rows.numel(),) if rows is not None else None, torch.int32, dev)
-    guard, stream = _launch_on(refs, "refs", stream)
-    with guard:
-        st = _load().kda_pages_free(_p(refs), refs.shape[0], _p(table), _p(counts), table.shape[0], table.shape[1],
-                                    _p(rows), rows.shape[0], ctypes.c_void_p(stream.cuda_stream))
-    _check(st, "kda_pages_free")
+    n_pages, n_rows, most = _book(refs, table, counts, dev)
+    _need(rows, "rows", None, torch.int32, dev)
+    _same(rows, "rows", (rows.numel(),), torch.int32, dev)
+    with _Launch(refs, "refs", stream) as on:
+        st = _load().kda_pages_free(refs.data_ptr(), n_pages, table.data_ptr(), counts.data_ptr(), n_rows, most,
+                                    rows.data_ptr(), rows.shape[0], on.raw)
+    if st:
+        _check(st, "kda_pages_free")
 
 
 def kda_pages_compact(pool, refs, table, counts, *, remap=None, n_live=None, workspace=None, stream=None):
@@ -542,25 +590,27 @@ def kda_pages_compact(pool, refs, table, counts, *, remap=None, n_live=None, wor
     here when None), n_live int32 [1] the number of pages in use.  Returns remap.
     """
     nb = _page_bytes(pool, "pool", 2)
-    dev = pool.device
-    _book(refs, table, counts, dev)
-    n_pages = pool.shape[1]
-    if refs.shape[0] != n_pages:
-        raise ValueError(f"refs: expected {n_pages} pages, got {refs.shape[0]}")
-    guard, stream = _launch_on(pool, "pool", stream)
-    if remap is None:
-        with torch.cuda.stream(stream):
-            remap = torch.empty(n_pages, dtype=torch.int32, device=dev)
-    _need(remap, "remap", (n_pages,), torch.int32, dev)
-    _opt(n_live, "n_live", (1,), torch.int32, dev)
-    if workspace is None:
-        workspace = _scratch(_load().kda_pages_compact_workspace_bytes(n_pages), dev, stream)
-    _need(workspace, "workspace", None, torch.uint8, dev)
-    with guard:
-        st = _load().kda_pages_compact(_p(pool), pool.shape[0], n_pages, nb, _p(refs), _p(table), _p(counts), table.shape[0],
-                                       table.shape[1], _p(remap), _p(n_live), _p(workspace), workspace.numel(),
-                                       ctypes.c_void_p(stream.cuda_stream))
-    _check(st, "kda_pages_compact")
+    dev, i32 = pool.device, torch.int32
+    n_pages, rows, most = _book(refs, table, counts, dev)
+    if n_pages != pool.shape[1]:
+        raise ValueError(f"refs: expected {pool.shape[1]} pages, got {n_pages}")
+    if n_live is not None:
+        _same(n_live, "n_live", (1,), i32, dev)
+    L = _load()
+    with _Launch(pool, "pool", stream) as on:
+        if remap is None:
+            remap = on.empty(n_pages, i32)
+        else:
+            _same(remap, "remap", (n_pages,), i32, dev)
+        if workspace is None:
+            workspace = on.empty(max(L.kda_pages_compact_workspace_bytes(n_pages), 256))
+        else:
+            _need(workspace, "workspace", None, torch.uint8, dev)
+        st = L.kda_pages_compact(pool.data_ptr(), pool.shape[0], n_pages, nb, refs.data_ptr(), table.data_ptr(),
+                                 counts.data_ptr(), rows, most, remap.data_ptr(), _ptr(n_live), workspace.data_ptr(),
+                                 workspace.numel(), on.raw)
+    if st:
+        _check(st, "kda_pages_compact")
     return remap
 
 

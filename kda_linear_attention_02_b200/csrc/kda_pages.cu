@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(1024) pages_fork_plan_kernel(int32_t* refs, in
             bool ok = c >= 0 && c < n_rows && p >= -1 && p < n_rows && fresh >= 0 && fresh <= max_pages;
             if (ok) {
                 e.have = p >= 0 ? counts[p] : 0;
-                e.keep = p == c ? e.have : p >= 0 ? n_shared[i] : 0;
+                e.keep = p == c ? e.have : p >= 0 && n_shared ? n_shared[i] : 0;
                 ok = e.have >= 0 && e.have <= max_pages && e.keep >= 0 && e.keep <= e.have && e.have + fresh <= max_pages &&
                      (p == c || counts[c] == 0) && !(atomicOr(&opened[c >> 5], 1u << (c & 31)) >> (c & 31) & 1u);
             }
@@ -506,8 +506,7 @@ kda_status_t kda_pages_fork(void* pool, int n_planes, int n_pages, size_t page_b
         static_cast<long long>(n) * max_pages > kMaxMoves || (zero_fresh != 0 && zero_fresh != 1))
         return KDA_ERR_ARG;
     if (n == 0) return KDA_OK;
-    if ((!pool && n_pages > 0) || (!refs && n_pages > 0) || !table || !counts || !parents || !children || !n_shared ||
-        !workspace)
+    if ((!pool && n_pages > 0) || (!refs && n_pages > 0) || !table || !counts || !parents || !children || !workspace)
         return KDA_ERR_ARG;
     const void* ints[] = {refs, table, counts, parents, children, n_shared, n_fresh};
     for (const void* p : ints)

@@ -103,7 +103,7 @@ def fork(lib, **over):
     (dict(n=-1), ARG), (dict(planes=0), ARG), (dict(np=-1), ARG), (dict(pb=8), ARG), (dict(rows=-1), ARG),
     (dict(rows=(1 << 20) + 1), ARG), (dict(most=0), ARG), (dict(zero=2), ARG), (dict(n=1 << 20, most=1 << 12), ARG),
     (dict(pool=None), ARG), (dict(refs=None), ARG), (dict(table=None), ARG), (dict(counts=None), ARG), (dict(p=None), ARG),
-    (dict(c=None), ARG), (dict(sh=None), ARG), (dict(ws=None), ARG), (dict(pool=0x100008), ALIGN), (dict(table=0x2001), ALIGN),
+    (dict(c=None), ARG), (dict(sh=0x6002), ALIGN), (dict(ws=None), ARG), (dict(pool=0x100008), ALIGN), (dict(table=0x2001), ALIGN),
     (dict(fr=0x7002), ALIGN), (dict(ws=0x10010), ALIGN), (dict(wsb=64), WORKSPACE)])
 def test_fork_refusals(lib, over, want):
     assert fork(lib, **over) == want
