@@ -18,12 +18,12 @@ namespace kda {
 
 namespace {
 
-// Splits the sequences into segments of seg_len tokens and validates cu_seqlens (cu[0] = 0, non-decreasing,
-// cu[N] = total); a bad table gives no items, so that the kernels behind do nothing.  When all items fit one
-// block they are ordered by length, longest first: blocks start in that order, and a long sequence that
-// started last would run on alone at the end.
+// Splits the sequences of more than `whole` tokens into segments of seg_len tokens and validates cu_seqlens
+// (cu[0] = 0, non-decreasing, cu[N] = total); a bad table gives no items, so that the kernels behind do
+// nothing.  When all items fit one block they are ordered by length, longest first: blocks start in that order,
+// and a long sequence that started last would run on alone at the end.
 __global__ void __launch_bounds__(1024) lin_index_kernel(const int32_t* __restrict__ cu, int n_seqs, int total,
-                                                         int seg_len, int max_items, LinHead* head, LinItem* items,
+                                                         int whole, int seg_len, LinHead* head, LinItem* items,
                                                          int2* multi, int* status) {
     __shared__ long long warp_sums[32];
     __shared__ int lens[1024];
@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(1024) lin_index_kernel(const int32_t* __restri
         if (i < n_seqs) {
             t0 = cu[i];
             len = cu[i + 1] - t0;
-            ns = len > seg_len ? (len - 1) / seg_len + 1 : 1;
+            ns = len > whole ? (len - 1) / seg_len + 1 : 1;
         }
         const long long c = ns ? (static_cast<long long>(ns - 1) << 32) | ns : 0;
         long long x = c;
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(1024) lin_index_kernel(const int32_t* __restri
         const long long first = carry + x - c + (w ? warp_sums[w - 1] : 0);
         const int item0 = static_cast<int>(first & 0xffffffff), z0 = static_cast<int>(first >> 32);
         for (int s = 0; s < ns; ++s)
-            items[item0 + s] = LinItem{i, s, ns, t0 + s * seg_len, min(seg_len, len - s * seg_len), s * seg_len, z0, 0};
+            items[item0 + s] = LinItem{i, s, ns, t0 + s * seg_len, ns == 1 ? len : min(seg_len, len - s * seg_len), s * seg_len, z0, 0};
         if (ns > 1) multi[atomicAdd(&s_multi, 1)] = make_int2(z0, ns);   // their order has no effect
         carry += warp_sums[31];
         __syncthreads();
@@ -138,23 +138,35 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) &
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 bool dims_ok(int dk, int dv) { return (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }
 
-// Tokens per segment.  No segment is longer than a fair share of the batch's (token, head) pairs over the
-// SMs, plus a quarter; none is shorter than kMinSeg, below which the extra pass costs more than it gives.
-constexpr int kSms = 148, kMinSeg = 1024;
-int segment_tokens(int64_t total_tokens, int H) {
-    const int64_t share = (total_tokens * H * 5 + kSms * 4 - 1) / (kSms * 4);
-    const int64_t len = std::max<int64_t>(kMinSeg, (share + kChunk - 1) / kChunk * kChunk);
-    return static_cast<int>(std::min<int64_t>(len, 0x40000000));
+// Which sequences are cut, and into segments of how many tokens.  A sequence stays whole when it has at most a
+// quarter more than a fair share of the batch's (token, head) pairs over the SMs: the cut costs a second
+// reading of k and v.  Else its segments have half a share, so that they fill the SMs about twice over, but at
+// least `least` tokens, below which a segment's set-up and the extra pass cost more than they give.
+constexpr int kSms = 148;
+struct SegRule {
+    int whole, len;
+};
+SegRule segment_rule(int64_t total_tokens, int H, int dv, bool bf16) {
+    // fp32: a CTA has 32 columns of a state, and walks about five times as slowly
+    const int64_t per_token = bf16 ? H : static_cast<int64_t>(H) * (dv / 32), least = bf16 ? 512 : 128;
+    const int64_t share = (total_tokens * per_token + kSms - 1) / kSms;
+    auto chunks = [](int64_t tokens) { return (tokens + kChunk - 1) / kChunk * kChunk; };
+    SegRule r{};
+    r.len = static_cast<int>(std::min<int64_t>(std::max<int64_t>(least, chunks(share / 2 + share / 32)), 0x40000000));
+    r.whole = static_cast<int>(std::min<int64_t>(std::max<int64_t>(2 * least, share + share / 4), 0x40000000));
+    return r;
 }
 
 struct LinLayout {
-    int seg_len, max_items, max_bounds;
+    SegRule seg;
+    int max_items, max_bounds;
     size_t items, multi, z, zdecay, total;
 };
-LinLayout layout(int64_t total_tokens, int n_seqs, int H, int dk, int dv) {
+LinLayout layout(int64_t total_tokens, int n_seqs, int H, int dk, int dv, bool bf16) {
     LinLayout l{};
-    l.seg_len = segment_tokens(total_tokens, H);
-    l.max_bounds = static_cast<int>(total_tokens / l.seg_len);   // every segment with a successor is full
+    l.seg = segment_rule(total_tokens, H, dv, bf16);
+    // a sequence that is cut has more than `whole` tokens, and every segment with a successor is full
+    l.max_bounds = total_tokens > l.seg.whole ? static_cast<int>(total_tokens / l.seg.len) : 0;
     l.max_items = n_seqs + l.max_bounds;
     size_t at = round256(sizeof(LinHead));
     auto take = [&](size_t bytes) {
@@ -182,7 +194,7 @@ size_t kda_lin_chunk_fwd_workspace_bytes(int64_t total_tokens, int n_seqs, int H
     if (total_tokens < 0 || total_tokens > 0x7fffffffLL || n_seqs < 0 || H <= 0 || !dims_ok(dk, dv)) return 0;
     if (dtype != KDA_BF16 && dtype != KDA_F32) return 0;
     if (n_seqs > 0x3fffffff) return 0;
-    return layout(total_tokens, n_seqs, H, dk, dv).total;
+    return layout(total_tokens, n_seqs, H, dk, dv, dtype == KDA_BF16).total;
 }
 
 kda_status_t kda_lin_chunk_fwd(const void* q, const void* k, const void* v, const float* log_alpha, int la_per_token,
@@ -206,7 +218,8 @@ kda_status_t kda_lin_chunk_fwd(const void* q, const void* k, const void* v, cons
     if ((log_alpha && !aligned(log_alpha, 4)) || !aligned(cu_seqlens, 4) || (ckpt_cu && !aligned(ckpt_cu, 4)))
         return KDA_ERR_ALIGN;
     if (!aligned(workspace, 256)) return KDA_ERR_ALIGN;
-    const LinLayout l = layout(total_tokens, n_seqs, H, dk, dv);
+    const bool bf16 = dtype == KDA_BF16;
+    const LinLayout l = layout(total_tokens, n_seqs, H, dk, dv, bf16);
     if (ws_bytes < l.total) return KDA_ERR_WORKSPACE;
     if (static_cast<long long>(l.max_items) * H > 0x7fffffffLL) return KDA_ERR_ARG;
 
@@ -221,14 +234,13 @@ kda_status_t kda_lin_chunk_fwd(const void* q, const void* k, const void* v, cons
     a.multi = reinterpret_cast<int2*>(ws + l.multi);
     a.z = reinterpret_cast<float*>(ws + l.z);
     a.zdecay = reinterpret_cast<float*>(ws + l.zdecay);
-    a.max_items = l.max_items; a.max_bounds = l.max_bounds; a.seg_len = l.seg_len;
+    a.max_items = l.max_items; a.max_bounds = l.max_bounds;
     a.status = status_ptr();
     if (!a.status) return KDA_ERR_CUDA;
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool bf16 = dtype == KDA_BF16;
     if (launch_chained(lin_index_kernel, dim3(1), dim3(1024), s, cu_seqlens, n_seqs, static_cast<int>(total_tokens),
-                       l.seg_len, l.max_items, a.head, a.items, a.multi, a.status) != cudaSuccess)
+                       l.seg.whole, l.seg.len, a.head, a.items, a.multi, a.status) != cudaSuccess)
         return KDA_ERR_CUDA;
     if (l.max_bounds > 0) {
         if ((bf16 ? launch_lin_bf16(a, true, s) : launch_lin_simt(a, true, s)) != cudaSuccess) return KDA_ERR_CUDA;

@@ -59,7 +59,6 @@ struct LinArgs {
     float* z;                    // [boundaries, H, dk, dv]
     float* zdecay;               // [boundaries, H]
     int max_items, max_bounds;   // bounds the host knows
-    int seg_len;                 // tokens per segment (a multiple of kChunk)
     int* status;
 };
 
