@@ -142,14 +142,13 @@ bool dims_ok(int dk, int dv) { return (dk == 64 || dk == 128) && (dv == 64 || dv
 // quarter more than a fair share of the batch's (token, head) pairs over the SMs: the cut costs a second
 // reading of k and v.  Else its segments have half a share, so that they fill the SMs about twice over, but at
 // least `least` tokens, below which a segment's set-up and the extra pass cost more than they give.
-constexpr int kSms = 148;
 struct SegRule {
     int whole, len;
 };
 SegRule segment_rule(int64_t total_tokens, int H, int dv, bool bf16) {
     // fp32: a CTA has 32 columns of a state, and walks about five times as slowly
     const int64_t per_token = bf16 ? H : static_cast<int64_t>(H) * (dv / 32), least = bf16 ? 512 : 128;
-    const int64_t share = (total_tokens * per_token + kSms - 1) / kSms;
+    const int64_t share = (total_tokens * per_token + kLinSms - 1) / kLinSms;
     auto chunks = [](int64_t tokens) { return (tokens + kChunk - 1) / kChunk * kChunk; };
     SegRule r{};
     r.len = static_cast<int>(std::min<int64_t>(std::max<int64_t>(least, chunks(share / 2 + share / 32)), 0x40000000));

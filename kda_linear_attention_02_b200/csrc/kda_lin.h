@@ -12,6 +12,8 @@ namespace kda {
 // alpha as it is and keeps sums of logarithms finite (minus infinity and NaN become -120 too).
 constexpr float kLinLogMin = -120.f;
 
+constexpr int kLinSms = 148;   // SMs of a B200
+
 // Lets the next kernel of the stream, launched with programmatic serialization, take its place on the SMs once
 // every block of this one has started; it still waits for this one's end before it touches memory.
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -32,8 +34,8 @@ struct __align__(16) LinItem {
 // head a state [dk, dv] and the decay of the segment ahead of it.
 struct __align__(16) LinHead {
     int n_items;
-    int n_multi;
-    int pad[2];
+    int n_multi;   // sequences with more than one segment
+    int next[2];   // (item, head) pairs taken from behind the grid's own, in the full and the boundary pass
 };
 
 struct LinArgs {

@@ -18,6 +18,9 @@
 // accumulator that lived on in tensor memory would collect the truncation of its additions over the length of
 // the sequence.
 //
+// The grid has a CTA per SM; each takes (segment, head) pairs from a counter, longest first, until none is left,
+// and its copies run ahead into the next pair while the last chunks of one are worked on.
+//
 // The warps are specialised and meet at mbarriers: a producer (TMA tiles of q, k, v, and the chunk's decays),
 // an issuer (all MMAs, in an order that keeps Z of one chunk ahead of the scores of the next), two warps for
 // P, four that split W, four that write o, four that hold the state.
@@ -64,6 +67,12 @@ constexpr int kPWarps = 2, kWWarps = 4, kOWarps = 4, kSWarps = 4;
 // Registers of a thread: 128 at launch; the warps that hold the state take 176, the others give theirs
 // (3 x 112 + 176 = 512, what four threads of the four groups were launched with).
 constexpr int kRegsState = 176, kRegsOther = 112;
+
+struct __align__(16) Job {   // a segment of one (sequence, head)
+    LinItem it;
+    int h;   // -1: there are no more
+    int pad[3];
+};
 
 struct Decays {            // of one chunk
     float g2[kChunk];      // g_t log2(e)
@@ -175,7 +184,8 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
     __shared__ Decays decays[F::ND];
     __shared__ __align__(8) float la_ring[4][C];
     __shared__ __align__(8) uint64_t full[NST], empty[NST], sp_full, sp_free, p_ready[2], p_free[2], w_go[2], w_free[2], z_free[2],
-        z_full[2], o_go, sb_free, o_full, done;
+        z_full[2], o_go, sb_free, o_full, done, job_full[2], job_free[2], w_sync, o_sync;
+    __shared__ Job jobs[2];
     __shared__ uint32_t tmem_slot;
     const int t = threadIdx.x, w = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
     if (t == 0) {
@@ -199,14 +209,18 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         mbar_init(&sb_free, 1);
         mbar_init(&o_full, 1);
         mbar_init(&done, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&job_full[b], 1);
+            mbar_init(&job_free[b], 1 + kWWarps + kSWarps + (BOUNDARY ? 0 : kPWarps + kOWarps));
+        }
+        mbar_init(&w_sync, kWWarps);
+        mbar_init(&o_sync, kOWarps);
         fence_barrier_init();
     }
     grid_launch_dependents();
     grid_dependency_wait();
-    const int item = blockIdx.x / a.H, h = blockIdx.x % a.H;
-    if (item >= a.head->n_items) return;
-    const LinItem it = a.items[item];
-    if (BOUNDARY && it.seg + 1 == it.n_seg) return;
+    const int n_jobs = a.head->n_items * a.H;
+    if (BOUNDARY ? a.head->n_multi == 0 : static_cast<int>(blockIdx.x) >= n_jobs) return;
     if (w == 3) {
         tmem_alloc(&tmem_slot, F::COLS);
         tmem_relinquish();
@@ -215,99 +229,143 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_slot;
-    const int nch = (it.n + C - 1) / C, hq = h / (a.H / a.Hqk);
     bool ok = true;   // no wait of this warp has run out
+    // The k-th pair of this CTA, for every warp but the producer; false behind the last.
+    auto next_job = [&](int k, LinItem& it, int& h) {
+        ok = ok && bar_wait(&job_full[k & 1], (k >> 1) & 1);
+        if (!ok) return false;
+        const Job& j = jobs[k & 1];
+        it = j.it;
+        h = j.h;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&job_free[k & 1]);
+        return h >= 0;
+    };
+    // Four warps meet (bounded, as all waits are; a named barrier would not be).
+    auto meet = [&](uint64_t* bar, int& n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+        ok = ok && bar_wait(bar, n & 1);
+        ++n;
+    };
 
     if (w < 4) {
         // every warp of a group of four changes its registers by the same instruction
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (w == 2) {
             // ---------------- producer
-            // log_alpha of this lane's tokens 2 lane and 2 lane + 1, three chunks ahead: a load takes longer than a
-            // chunk.  Copied to shared memory, since moving a value on in registers would wait for its load.
-            const float* la = a.la + (static_cast<size_t>(it.t0) + 2 * lane) * a.la_t + h;
-            const uint32_t la_at = smem_u32(&la_ring[0][2 * lane]);
-            int left = it.n - 2 * lane;   // tokens of the segment from the lane's first one on
-            auto fetch = [&](int c) {
-                const uint32_t at = la_at + (c & 3) * static_cast<uint32_t>(sizeof(la_ring[0]));
-                cp_async4(at, left > 0 ? la : a.la, left > 0);
-                cp_async4(at + 4, left > 1 ? la + a.la_t : a.la, left > 1);
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                la += C * static_cast<size_t>(a.la_t);
-                left -= C;
+            // Claims a pair: the CTA's own number first, then from the counter; lane 0.
+            auto claim = [&](bool first, Job& j) {
+                auto count = [&]() { return static_cast<int>(gridDim.x) + atomicAdd(&a.head->next[BOUNDARY], 1); };
+                for (int x = first ? static_cast<int>(blockIdx.x) : count();; x = count()) {
+                    j.h = -1;
+                    if (x >= n_jobs) return;
+                    j.it = a.items[x / a.H];
+                    if (BOUNDARY && j.it.seg + 1 == j.it.n_seg) continue;
+                    j.h = x % a.H;
+                    return;
+                }
             };
-            float total = 0.f;
-            if (nch > 0)
+            Job next;
+            if (lane == 0) claim(true, next);
+            int s = 0, ph = 1, g = 0;   // stage and its parity, chunks so far
 #pragma unroll 1
-                for (int c = 0; c < 3; ++c) fetch(c);
-            int s = 0, ph = 1, issued = 0;
-#pragma unroll 1
-            for (int c = 0; c < nch; ++c) {
-                if (!(ok = bar_wait(&empty[s], ph))) break;
-                if (lane == 0) {
-                    uint8_t* sb = sm + s * F::STAGE;
-                    mbar_arrive_expect_tx(&full[s], F::STAGE);
-                    const int tok = it.t0 + c * C;
-#pragma unroll 1
-                    for (int b = 0; b < DK / 64; ++b) {
-                        if (!BOUNDARY) tma_load_2d(sb + b * F::HALF, &mq, hq * DK + 64 * b, tok, &full[s]);
-                        tma_load_2d(sb + F::QB + b * F::HALF, &mk, hq * DK + 64 * b, tok, &full[s]);
-                    }
-#pragma unroll 1
-                    for (int b = 0; b < DV / 64; ++b)
-                        tma_load_2d(sb + F::QB + F::KB + b * F::HALF, &mv, h * DV + 64 * b, tok, &full[s]);
-                }
-                issued = c + 1;
-                fetch(c + 3);
-                asm volatile("cp.async.wait_group 3;" ::: "memory");
-                const float2 x = *reinterpret_cast<const float2*>(&la_ring[c & 3][2 * lane]);
-                const bool in0 = c * C + 2 * lane < it.n, in1 = c * C + 2 * lane + 1 < it.n;
-                const float x0 = in0 ? fmaxf(x.x, kLinLogMin) : 0.f, x1 = in1 ? fmaxf(x.y, kLinLogMin) : 0.f;
-                // inclusive sums of the lanes' pairs, from the chunk's start and from its end
-                float f = x0 + x1, r = f;
-#pragma unroll 1
-                for (int off = 1; off < 32; off <<= 1) {
-                    const float u = __shfl_up_sync(0xffffffffu, f, off), v = __shfl_down_sync(0xffffffffu, r, off);
-                    if (lane >= off) f += u;
-                    if (lane + off < 32) r += v;
-                }
-                float before = __shfl_up_sync(0xffffffffu, f, 1), after = __shfl_down_sync(0xffffffffu, r, 1);
-                if (lane == 0) before = 0.f;
-                if (lane == 31) after = 0.f;
-                const float sum = __shfl_sync(0xffffffffu, f, 31), gm = __shfl_sync(0xffffffffu, f, 15);
-                Decays& d = decays[c % F::ND];
-                const float2 g = make_float2(before + x0, f);
-                *reinterpret_cast<float2*>(&d.g2[2 * lane]) = make_float2(g.x * kLog2e, g.y * kLog2e);
-                *reinterpret_cast<float2*>(&d.eg[2 * lane]) = make_float2(exp_fast(g.x), exp_fast(g.y));
-                float w0 = exp_fast(after + x1), w1 = exp_fast(after);
-                uint32_t part[3];
-#pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    part[k] = pack_bf16x2(w0, w1);
-                    w0 -= lo_f32(part[k]);
-                    w1 -= hi_f32(part[k]);
-                }
-                d.w[lane] = make_uint4(part[0], part[1], part[2] ^ 0x80008000u, 0u);
-                if (lane < 16)
-                    *reinterpret_cast<float2*>(&d.m[2 * lane]) =
-                        make_float2(ex2_approx((gm - g.x) * kLog2e), ex2_approx((gm - g.y) * kLog2e));
-                if (lane == 0) {
-                    d.g2m = gm * kLog2e;
-                    d.eC = exp_fast(sum);
-                }
-                total += sum;
+            for (int k = 0; ok; ++k) {
+                if (k >= 2 && !(ok = bar_wait(&job_free[k & 1], ((k >> 1) - 1) & 1))) break;
+                if (lane == 0) jobs[k & 1] = next;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&full[s]);
-                if (++s == NST) {
-                    s = 0;
-                    ph ^= 1;
+                const LinItem it = jobs[k & 1].it;
+                const int h = jobs[k & 1].h;
+                if (lane == 0) mbar_arrive(&job_full[k & 1]);
+                if (h < 0) break;
+                const int nch = (it.n + C - 1) / C, hq = h / (a.H / a.Hqk);
+                // log_alpha of this lane's tokens 2 lane and 2 lane + 1, three chunks ahead: a load takes longer than
+                // a chunk.  Copied to shared memory, since moving a value on in registers would wait for its load.
+                const float* la = a.la + (static_cast<size_t>(it.t0) + 2 * lane) * a.la_t + h;
+                const uint32_t la_at = smem_u32(&la_ring[0][2 * lane]);
+                int left = it.n - 2 * lane;   // tokens of the segment from the lane's first one on
+                auto fetch = [&](int c) {
+                    const uint32_t at = la_at + (c & 3) * static_cast<uint32_t>(sizeof(la_ring[0]));
+                    cp_async4(at, left > 0 ? la : a.la, left > 0);
+                    cp_async4(at + 4, left > 1 ? la + a.la_t : a.la, left > 1);
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    la += C * static_cast<size_t>(a.la_t);
+                    left -= C;
+                };
+                float total = 0.f;
+                if (nch > 0)
+#pragma unroll 1
+                    for (int c = 0; c < 3; ++c) fetch(c);
+#pragma unroll 1
+                for (int c = 0; c < nch; ++c, ++g) {
+                    if (!(ok = bar_wait(&empty[s], ph))) break;
+                    if (lane == 0) {
+                        uint8_t* sb = sm + s * F::STAGE;
+                        mbar_arrive_expect_tx(&full[s], F::STAGE);
+                        const int tok = it.t0 + c * C;
+#pragma unroll 1
+                        for (int b = 0; b < DK / 64; ++b) {
+                            if (!BOUNDARY) tma_load_2d(sb + b * F::HALF, &mq, hq * DK + 64 * b, tok, &full[s]);
+                            tma_load_2d(sb + F::QB + b * F::HALF, &mk, hq * DK + 64 * b, tok, &full[s]);
+                        }
+#pragma unroll 1
+                        for (int b = 0; b < DV / 64; ++b)
+                            tma_load_2d(sb + F::QB + F::KB + b * F::HALF, &mv, h * DV + 64 * b, tok, &full[s]);
+                    }
+                    fetch(c + 3);
+                    asm volatile("cp.async.wait_group 3;" ::: "memory");
+                    const float2 x = *reinterpret_cast<const float2*>(&la_ring[c & 3][2 * lane]);
+                    const bool in0 = c * C + 2 * lane < it.n, in1 = c * C + 2 * lane + 1 < it.n;
+                    const float x0 = in0 ? fmaxf(x.x, kLinLogMin) : 0.f, x1 = in1 ? fmaxf(x.y, kLinLogMin) : 0.f;
+                    // inclusive sums of the lanes' pairs, from the chunk's start and from its end
+                    float f = x0 + x1, r = f;
+#pragma unroll 1
+                    for (int off = 1; off < 32; off <<= 1) {
+                        const float u = __shfl_up_sync(0xffffffffu, f, off), v = __shfl_down_sync(0xffffffffu, r, off);
+                        if (lane >= off) f += u;
+                        if (lane + off < 32) r += v;
+                    }
+                    float before = __shfl_up_sync(0xffffffffu, f, 1), after = __shfl_down_sync(0xffffffffu, r, 1);
+                    if (lane == 0) before = 0.f;
+                    if (lane == 31) after = 0.f;
+                    const float sum = __shfl_sync(0xffffffffu, f, 31), gm = __shfl_sync(0xffffffffu, f, 15);
+                    Decays& d = decays[g % F::ND];
+                    const float2 gt = make_float2(before + x0, f);
+                    *reinterpret_cast<float2*>(&d.g2[2 * lane]) = make_float2(gt.x * kLog2e, gt.y * kLog2e);
+                    *reinterpret_cast<float2*>(&d.eg[2 * lane]) = make_float2(exp_fast(gt.x), exp_fast(gt.y));
+                    float w0 = exp_fast(after + x1), w1 = exp_fast(after);
+                    uint32_t part[3];
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) {
+                        part[p] = pack_bf16x2(w0, w1);
+                        w0 -= lo_f32(part[p]);
+                        w1 -= hi_f32(part[p]);
+                    }
+                    d.w[lane] = make_uint4(part[0], part[1], part[2] ^ 0x80008000u, 0u);
+                    if (lane < 16)
+                        *reinterpret_cast<float2*>(&d.m[2 * lane]) =
+                            make_float2(ex2_approx((gm - gt.x) * kLog2e), ex2_approx((gm - gt.y) * kLog2e));
+                    if (lane == 0) {
+                        d.g2m = gm * kLog2e;
+                        d.eC = exp_fast(sum);
+                    }
+                    total += sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[s]);
+                    if (++s == NST) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                    // late, so that a CTA with a long pair does not sit on another
+                    if (c == max(nch - 2, 0) && lane == 0) claim(false, next);
                 }
+                if (BOUNDARY && lane == 0) a.zdecay[static_cast<size_t>(it.z0 + it.seg) * a.H + h] = exp_fast(total);
+                if (nch == 0 && lane == 0) claim(false, next);
+                cp_async_wait_all();   // before the ring is filled anew
             }
-            if (BOUNDARY && lane == 0) a.zdecay[static_cast<size_t>(it.z0 + it.seg) * a.H + h] = exp_fast(total);
-            cp_async_wait_all();
             // no copy stays in flight behind the CTA: wait (bounded, quietly) for the last fill of every stage
-    #pragma unroll 1
-        for (int c = issued > NST ? issued - NST : 0; c < issued; ++c) bar_wait(&full[c % NST], (c / NST) & 1);
+#pragma unroll 1
+            for (int c = g > NST ? g - NST : 0; c < g; ++c) bar_wait(&full[c % NST], (c / NST) & 1);
         } else if (w == 3) {
             // ---------------- issuer
             constexpr uint32_t id_o = idesc_bf16(128, C), id_o2 = idesc_bf16(128, C, false, false, true),
@@ -322,58 +380,67 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 for (int i = 0; i < DK / 16; ++i) mma_ss(tmu + F::SP, qd + slice(i), kd + slice(i), id_o, i > 0);
                 mma_commit(&sp_full);
             };
-            if (!BOUNDARY && nch > 0 && (ok = bar_wait(&full[0], 0))) scores(0);
-            int s = 0, ph = 0;   // stage of chunk c, and the parity of its use
+            int s = 0, ph = 0, g = 0;   // stage and its parity, chunks so far
+            LinItem it;
+            int h;
 #pragma unroll 1
-            for (int c = 0; ok && c < nch; ++c) {
-                const uint32_t q = base + s * F::STAGE, k = q + F::QB, v = k + F::KB;
-                const int s1 = s + 1 == NST ? 0 : s + 1, ph1 = s + 1 == NST ? ph ^ 1 : ph;
-                if (BOUNDARY && !(ok = bar_wait(&full[s], ph))) break;
-                // Z in two halves of the chunk's tokens, so that the warps of W fill one half while the other is used
-                const uint64_t kd = sdesc_mn_sw128(k, F::HALF);
-                const uint32_t zcol = tmu + F::Z + (c % F::NZ) * 128;
-                auto z_half = [&](int half) {
+            for (int job = 0; ok && next_job(job, it, h); ++job) {
+                const int nch = (it.n + C - 1) / C;
+                // the scores are formed a chunk ahead, but not ahead of the pair
+                if (!BOUNDARY && nch > 0) {
+                    if (!(ok = bar_wait(&full[s], ph) && (g == 0 || bar_wait(&sp_free, (g - 1) & 1)))) break;
                     tc_fence_after();
+                    scores(s);
+                }
 #pragma unroll 1
-                    for (int i = 0; i < 8; ++i) {   // part i / 2, tokens 32 half + 16 (i % 2) ..; the odd parts are negated
-                        const int sl = 2 * half + (i & 1);
-                        mma_ts(zcol, tmu + F::W + 32 * (i >> 1) + 8 * sl, kd + sl * (2048 >> 4), id_z | ((i & 2) ? neg_a : 0u),
-                               half + i > 0);
+                for (int c = 0; c < nch; ++c, ++g) {
+                    const uint32_t q = base + s * F::STAGE, k = q + F::QB, v = k + F::KB;
+                    const int s1 = s + 1 == NST ? 0 : s + 1, ph1 = s + 1 == NST ? ph ^ 1 : ph;
+                    if (BOUNDARY && !(ok = bar_wait(&full[s], ph))) break;
+                    // Z in two halves of the chunk's tokens, so that the warps of W fill one half while the other is used
+                    const uint64_t kd = sdesc_mn_sw128(k, F::HALF);
+                    const uint32_t zcol = tmu + F::Z + (g % F::NZ) * 128;
+                    auto z_half = [&](int half) {
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int i = 0; i < 8; ++i) {   // part i / 2, tokens 32 half + 16 (i % 2) ..; odd parts are negated
+                            const int sl = 2 * half + (i & 1);
+                            mma_ts(zcol, tmu + F::W + 32 * (i >> 1) + 8 * sl, kd + sl * (2048 >> 4), id_z | ((i & 2) ? neg_a : 0u),
+                                   half + i > 0);
+                        }
+                        mma_commit(&w_free[half]);
+                    };
+                    if (!(ok = bar_wait(&w_go[0], g & 1) &&
+                               (g < F::NZ || bar_wait(&z_free[g % F::NZ], (g / F::NZ - 1) & 1))))
+                        break;
+                    z_half(0);
+                    if (!BOUNDARY && c + 1 < nch) {
+                        if (!(ok = bar_wait(&full[s1], ph1) && bar_wait(&sp_free, g & 1))) break;
+                        tc_fence_after();
+                        scores(s1);
                     }
-                    mma_commit(&w_free[half]);
-                };
-                if (!(ok = bar_wait(&w_go[0], c & 1) &&
-                           (c < F::NZ || bar_wait(&z_free[c % F::NZ], (c / F::NZ - 1) & 1))))
-                    break;
-                z_half(0);
-                if (!BOUNDARY && c + 1 < nch) {
-                    if (!(ok = bar_wait(&full[s1], ph1) && bar_wait(&sp_free, c & 1))) break;
-                    tc_fence_after();
-                    scores(s1);
-                }
-                if (!(ok = bar_wait(&w_go[1], c & 1))) break;
-                z_half(1);
-                mma_commit(&z_full[c & 1]);
-                if (!BOUNDARY) {
-                    if (!(ok = bar_wait(&o_go, c & 1))) break;
-                    tc_fence_after();
-                    const uint64_t qd = sdesc_k_sw128(q);
+                    if (!(ok = bar_wait(&w_go[1], g & 1))) break;
+                    z_half(1);
+                    mma_commit(&z_full[g & 1]);
+                    if (!BOUNDARY) {
+                        if (!(ok = bar_wait(&o_go, g & 1))) break;
+                        tc_fence_after();
+                        const uint64_t qd = sdesc_k_sw128(q);
 #pragma unroll
-                    for (int i = 0; i < DK / 16; ++i) mma_ts(tmu + F::O1, tmu + F::SB + 8 * i, qd + slice(i), id_o, i > 0);
-                    mma_commit(&sb_free);
-                    if (!(ok = bar_wait(&p_ready[c & 1], (c >> 1) & 1))) break;
-                    tc_fence_after();
-                    const uint64_t vd = sdesc_mn_sw128(v, F::HALF), pd = sdesc_k_sw128(base + F::P0 + (c & 1) * F::PB);
+                        for (int i = 0; i < DK / 16; ++i) mma_ts(tmu + F::O1, tmu + F::SB + 8 * i, qd + slice(i), id_o, i > 0);
+                        mma_commit(&sb_free);
+                        if (!(ok = bar_wait(&p_ready[g & 1], (g >> 1) & 1))) break;
+                        tc_fence_after();
+                        const uint64_t vd = sdesc_mn_sw128(v, F::HALF), pd = sdesc_k_sw128(base + F::P0 + (g & 1) * F::PB);
 #pragma unroll
-                    for (int i = 0; i < C / 16; ++i) mma_ss(tmu + F::O2, vd + i * (2048 >> 4), pd + i * 2, id_o2, i > 0);
-                    mma_commit(&o_full);
-                    mma_commit(&p_free[c & 1]);
+                        for (int i = 0; i < C / 16; ++i) mma_ss(tmu + F::O2, vd + i * (2048 >> 4), pd + i * 2, id_o2, i > 0);
+                        mma_commit(&o_full);
+                        mma_commit(&p_free[g & 1]);
+                    }
                     mma_commit(&empty[s]);
-                } else {
-                    mma_commit(&empty[s]);
+                    s = s1;
+                    ph = ph1;
                 }
-                s = s1;
-                ph = ph1;
             }
             mma_commit(&done);
             ok = bar_wait(&done, 0) && ok;   // no product stays in flight behind the CTA
@@ -395,16 +462,20 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 uint32_t mask[16];   // of the diagonal block's pairs: columns up to the row's own
 #pragma unroll
                 for (int j = 0; j < 16; ++j) mask[j] = 2 * j + 1 <= lane ? 0xffffffffu : 2 * j <= lane ? 0x0000ffffu : 0u;
-                int s = 0, ph = 0;
+                int s = 0, ph = 0, g = 0;
+                LinItem it;
+                int h;
 #pragma unroll 1
-                for (int c = 0; c < nch; ++c) {
-                    if (!(ok = bar_wait(&full[s], ph) && bar_wait(&sp_full, c & 1))) break;
+                for (int job = 0; ok && next_job(job, it, h); ++job)
+#pragma unroll 1
+                for (int c = (it.n + C - 1) / C; c > 0; --c, ++g) {
+                    if (!(ok = bar_wait(&full[s], ph) && bar_wait(&sp_full, g & 1))) break;
                     tc_fence_after();
-                    const Decays& d = decays[c % F::ND];
+                    const Decays& d = decays[g % F::ND];
                     const float gr = d.g2[row];
                     const uint32_t at = tm + F::SP + (static_cast<uint32_t>(32 * w) << 16);
-                    if (c >= 2 && !(ok = bar_wait(&p_free[c & 1], ((c >> 1) - 1) & 1))) break;
-                    uint8_t* p = p0 + (c & 1) * F::PB;
+                    if (g >= 2 && !(ok = bar_wait(&p_free[g & 1], ((g >> 1) - 1) & 1))) break;
+                    uint8_t* p = p0 + (g & 1) * F::PB;
                     // sixteen columns a turn: left of the diagonal block (second warp) the factor is a product of
                     // two, each at most 1, about g_32
                     const float er = ex2_approx(gr - d.g2m);
@@ -428,10 +499,10 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     tmem_wait_ld_regs<32>(x);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {   // what lies above the diagonal is cut off after the packing
-                        const float4 g = *reinterpret_cast<const float4*>(&d.g2[32 * w + j]);
-                        u[j / 2] = mask[j / 2] & pack_bf16x2(x[j] * ex2_approx(gr - g.x), x[j + 1] * ex2_approx(gr - g.y));
+                        const float4 gj = *reinterpret_cast<const float4*>(&d.g2[32 * w + j]);
+                        u[j / 2] = mask[j / 2] & pack_bf16x2(x[j] * ex2_approx(gr - gj.x), x[j + 1] * ex2_approx(gr - gj.y));
                         u[j / 2 + 1] =
-                            mask[j / 2 + 1] & pack_bf16x2(x[j + 2] * ex2_approx(gr - g.z), x[j + 3] * ex2_approx(gr - g.w));
+                            mask[j / 2 + 1] & pack_bf16x2(x[j + 2] * ex2_approx(gr - gj.z), x[j + 3] * ex2_approx(gr - gj.w));
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -442,7 +513,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     if (lane == 0) mbar_arrive(&sp_free);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_ready[c & 1]);
+                    if (lane == 0) mbar_arrive(&p_ready[g & 1]);
                     if (++s == NST) {
                         s = 0;
                         ph ^= 1;
@@ -463,22 +534,24 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             return (c8 >> 6) * F::HALF + tok * 128 + ((((c8 & 63) >> 3) ^ (tok & 7)) << 4);
         };
         const uint32_t row0 = tile_row(0), row1 = tile_row(1);
-        // A wait that runs out ends this warp's work, but not its part in the four warps' own barrier.
         auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && bar_wait(bar, parity); };
-        int s = 0, ph = 0;
+        int s = 0, ph = 0, g = 0, met = 0;
+        LinItem it;
+        int h;
         if (w < 8) {
             // ---------------- W
 #pragma unroll 1
-            for (int c = 0; c < nch; ++c) {
+            for (int job = 0; ok && next_job(job, it, h); ++job)
+#pragma unroll 1
+            for (int left = it.n; left > 0 && ok; left -= C, ++g) {
                 wait(&full[s], ph);
                 uint8_t* kt = sm + s * F::STAGE + F::QB;
                 uint8_t* vt = kt + F::KB;
-                const int n = it.n - c * C;
-                if (n < C) {
+                if (left < C) {
                     // rows behind the sequence belong to others: they must not reach a sum, not even times zero
 #pragma unroll 1
-                    for (int i = tg; ok && i < (C - n) * 8; i += 128) {
-                        const int r = n + i / 8, x = r * 128 + (i & 7) * 16;
+                    for (int i = tg; ok && i < (C - left) * 8; i += 128) {
+                        const int r = left + i / 8, x = r * 128 + (i & 7) * 16;
 #pragma unroll
                         for (int b = 0; b < DK / 64; ++b)
                             *reinterpret_cast<uint4*>(kt + b * F::HALF + x) = make_uint4(0u, 0u, 0u, 0u);
@@ -487,9 +560,9 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                             *reinterpret_cast<uint4*>(vt + b * F::HALF + x) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
-                    named_bar_sync(1, 128);
+                    meet(&w_sync, met);
                 }
-                const Decays& d = decays[c % F::ND];
+                const Decays& d = decays[g % F::ND];
                 uint32_t v[2][4];
                 uint4 wb[4];   // w1, w2, -w3 of this thread's pair of tokens in each block of eight
                 auto load_v = [&](uint32_t row, int half) {
@@ -517,7 +590,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                             if (lh == 0) load_v(row1, half);
                             else if (half == 0) load_v(row0, 32);
                         }
-                        if (lh == 0 && c > 0) wait(&w_free[half >> 5], (c - 1) & 1);
+                        if (lh == 0 && g > 0) wait(&w_free[half >> 5], (g - 1) & 1);
                         if (mine && ok) {
                             tc_fence_after();
 #pragma unroll
@@ -549,18 +622,20 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 __syncwarp();
                 if (lane == 0 && ok) mbar_arrive(&o_go);
             };
-            if (nch > 0) leave();
 #pragma unroll 1
-            for (int c = 0; c < nch; ++c) {
-                const int n = it.n - c * C;
-                wait(&o_full, c & 1);
-                uint8_t* ob = sm + F::O0 + (c & 1) * F::VB;
+            for (int job = 0; ok && next_job(job, it, h); ++job) {
+            if (it.n > 0) leave();
+#pragma unroll 1
+            for (int left = it.n; left > 0 && ok; left -= C, ++g) {
+                const int tok = it.t0 + it.n - left;
+                wait(&o_full, g & 1);
+                uint8_t* ob = sm + F::O0 + (g & 1) * F::VB;
                 // the store that read this buffer two chunks ago is done with it
                 if (tg == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                named_bar_sync(2, 128);
+                meet(&o_sync, met);
                 if (mine && ok) {
                     tc_fence_after();
-                    const Decays& d = decays[c % F::ND];
+                    const Decays& d = decays[g % F::ND];
 #pragma unroll 1
                     for (int u4 = 0; u4 < 4; ++u4) {   // 16 channels, 32 tokens
                         const int lh = u4 & 1, half = (u4 >> 1) * 32;
@@ -588,24 +663,24 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     tc_fence_before();
                 }
                 fence_proxy_async_smem();
-                if (c + 1 < nch) leave();
-                named_bar_sync(2, 128);
-                if (n >= C) {
+                if (left > C) leave();
+                meet(&o_sync, met);
+                if (left >= C) {
                     if (tg == 0 && ok) {
 #pragma unroll
-                        for (int b = 0; b < DV / 64; ++b) tma_store_2d(&mo, h * DV + 64 * b, it.t0 + c * C, ob + b * F::HALF);
+                        for (int b = 0; b < DV / 64; ++b) tma_store_2d(&mo, h * DV + 64 * b, tok, ob + b * F::HALF);
                         bulk_commit();
                     }
                 } else {   // the rows behind the sequence are not this one's to write
-                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) +
-                                         (static_cast<size_t>(it.t0) + c * C) * a.H * DV + static_cast<size_t>(h) * DV;
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + (static_cast<size_t>(tok) * a.H + h) * DV;
 #pragma unroll 1
-                    for (int i = tg; ok && i < n * (DV / 8); i += 128) {
+                    for (int i = tg; ok && i < left * (DV / 8); i += 128) {
                         const int r = i / (DV / 8), k8 = i % (DV / 8);
                         st_global_v4(dst + static_cast<size_t>(r) * a.H * DV + 8 * k8,
                                      *reinterpret_cast<const uint4*>(ob + (k8 >> 3) * F::HALF + r * 128 + (((k8 & 7) ^ (r & 7)) << 4)));
                     }
                 }
+            }
             }
             if (tg == 0) bulk_wait0();
         }
@@ -616,14 +691,6 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         const bool mine = ch < DV;
         const uint32_t lanes = static_cast<uint32_t>(32 * q4) << 16;
         float S[DK];
-        const float* start = nullptr;
-        if (it.seg == 0) {
-            if (a.initial_state) start = a.initial_state + (static_cast<size_t>(it.seq) * a.H + h) * DK * DV;
-        } else if (!BOUNDARY) {
-            start = a.z + (static_cast<size_t>(it.z0 + it.seg - 1) * a.H + h) * DK * DV;
-        }
-#pragma unroll
-        for (int i = 0; i < DK; ++i) S[i] = start && mine ? start[i * DV + ch] : 0.f;
         auto publish = [&]() {   // the bf16 copy that O1 multiplies q with
             if (mine) {
 #pragma unroll
@@ -639,69 +706,86 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_go);
         };
-        float* end = nullptr;
-        if (BOUNDARY) end = a.z + (static_cast<size_t>(it.z0 + it.seg) * a.H + h) * DK * DV;
-        else if (a.final_state && it.seg + 1 == it.n_seg)
-            end = a.final_state + (static_cast<size_t>(it.seq) * a.H + h) * DK * DV;
-        if (nch == 0 && end && mine)   // no tokens: the state stays as it was
+        int s = 0, ph = 0, g = 0;
+        LinItem it;
+        int h;
 #pragma unroll 1
-            for (int i = 0; i < DK; ++i) end[i * DV + ch] = start ? start[i * DV + ch] : 0.f;
-        // tokens to the next checkpoint, and its place
-        int to_ck = 0x7fffffff, ck = 0;
-        if (!BOUNDARY && a.ckpt_stride) {
-            to_ck = a.ckpt_stride - it.pos % a.ckpt_stride;
-            ck = a.ckpt_cu[it.seq] + it.pos / a.ckpt_stride;
-        }
-        int s = 0, ph = 0;
-#pragma unroll 1
-        for (int c = 0; c < nch; ++c) {
-            if (!(ok = bar_wait(&full[s], ph))) break;   // before Sb lets the chunk's products go ahead (see `leave`)
-            const float eC = decays[c % F::ND].eC;
-            if (BOUNDARY) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[s]);
-            } else {
-                if (c > 0 && !(ok = bar_wait(&sb_free, (c - 1) & 1))) break;   // the copy of the chunk before has been read
-                tc_fence_after();
-                publish();
+        for (int job = 0; ok && next_job(job, it, h); ++job) {
+            const float* start = nullptr;
+            if (it.seg == 0) {
+                if (a.initial_state) start = a.initial_state + (static_cast<size_t>(it.seq) * a.H + h) * DK * DV;
+            } else if (!BOUNDARY) {
+                start = a.z + (static_cast<size_t>(it.z0 + it.seg - 1) * a.H + h) * DK * DV;
             }
-            if (!(ok = bar_wait(&z_full[c & 1], (c >> 1) & 1))) break;
-            if (mine) {
-                tc_fence_after();
+            float* end = nullptr;
+            if (BOUNDARY) end = a.z + (static_cast<size_t>(it.z0 + it.seg) * a.H + h) * DK * DV;
+            else if (a.final_state && it.seg + 1 == it.n_seg)
+                end = a.final_state + (static_cast<size_t>(it.seq) * a.H + h) * DK * DV;
+            if (it.n == 0) {   // no tokens: the state stays as it was
+                if (end && mine)
+#pragma unroll 1
+                    for (int i = 0; i < DK; ++i) end[i * DV + ch] = start ? start[i * DV + ch] : 0.f;
+                continue;
+            }
 #pragma unroll
-                for (int b = 0; b < DK; b += 32) {
-                    float z[32];
-                    tmem_ld32(tm + lanes + F::Z + (c % F::NZ) * 128 + b, z);
-                    tmem_wait_ld_regs<32>(z);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) S[b + i] = fmaf(eC, S[b + i], z[i]);
+            for (int i = 0; i < DK; ++i) S[i] = start && mine ? start[i * DV + ch] : 0.f;
+            // tokens to the next checkpoint, and its place
+            int to_ck = 0x7fffffff, ck = 0;
+            if (!BOUNDARY && a.ckpt_stride) {
+                to_ck = a.ckpt_stride - it.pos % a.ckpt_stride;
+                ck = a.ckpt_cu[it.seq] + it.pos / a.ckpt_stride;
+            }
+#pragma unroll 1
+            for (int left = it.n; left > 0; left -= C, ++g) {
+                if (!(ok = bar_wait(&full[s], ph))) break;   // before Sb lets the chunk's products go ahead (see `leave`)
+                const float eC = decays[g % F::ND].eC;
+                if (BOUNDARY) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&empty[s]);
+                } else {
+                    if (g > 0 && !(ok = bar_wait(&sb_free, (g - 1) & 1))) break;   // the copy before has been read
+                    tc_fence_after();
+                    publish();
                 }
-                tc_fence_before();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&z_free[c % F::NZ]);
-            // a checkpoint, and the state at the segment's end
-            float* dst = nullptr;
-            to_ck -= C;
-            if (!BOUNDARY && to_ck == 0 && (c + 1) * C <= it.n) {
-                to_ck = a.ckpt_stride;
-                if (ck >= 0 && ck < a.ckpt_cu[it.seq + 1])
-                    dst = a.checkpoints + (static_cast<size_t>(ck) * a.H + h) * DK * DV;
-                else if (lane == 0)
-                    set_status(a.status, KDA_ERR_DEVICE_INPUT);
-                ++ck;
-            }
-            if (++s == NST) {
-                s = 0;
-                ph ^= 1;
-            }
-            if (mine && (dst || (end && c + 1 == nch))) {
-#pragma unroll 1
-                for (int k = 0; k < 2; ++k) {
-                    float* p = k == 0 ? dst : c + 1 == nch ? end : nullptr;
-                    if (p)
+                if (!(ok = bar_wait(&z_full[g & 1], (g >> 1) & 1))) break;
+                if (mine) {
+                    tc_fence_after();
 #pragma unroll
-                        for (int i = 0; i < DK; ++i) p[i * DV + ch] = S[i];
+                    for (int b = 0; b < DK; b += 32) {
+                        float z[32];
+                        tmem_ld32(tm + lanes + F::Z + (g % F::NZ) * 128 + b, z);
+                        tmem_wait_ld_regs<32>(z);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) S[b + i] = fmaf(eC, S[b + i], z[i]);
+                    }
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&z_free[g % F::NZ]);
+                if (++s == NST) {
+                    s = 0;
+                    ph ^= 1;
+                }
+                // a checkpoint, and the state at the segment's end
+                float* dst = nullptr;
+                to_ck -= C;
+                if (!BOUNDARY && to_ck == 0 && left >= C) {
+                    to_ck = a.ckpt_stride;
+                    if (ck >= 0 && ck < a.ckpt_cu[it.seq + 1])
+                        dst = a.checkpoints + (static_cast<size_t>(ck) * a.H + h) * DK * DV;
+                    else if (lane == 0)
+                        set_status(a.status, KDA_ERR_DEVICE_INPUT);
+                    ++ck;
+                }
+                float* const last = left <= C ? end : nullptr;
+                if (mine && (dst || last)) {
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {
+                        float* p = k == 0 ? dst : last;
+                        if (p)
+#pragma unroll
+                            for (int i = 0; i < DK; ++i) p[i * DV + ch] = S[i];
+                    }
                 }
             }
         }
@@ -742,7 +826,8 @@ cudaError_t launch(const LinArgs& a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(lin_bf16_kernel<DK, DV, BOUNDARY>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.max_items * a.H));
+    const long long jobs = static_cast<long long>(BOUNDARY ? a.max_bounds : a.max_items) * a.H;
+    cfg.gridDim = dim3(static_cast<unsigned>(jobs < kLinSms ? jobs : kLinSms));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
