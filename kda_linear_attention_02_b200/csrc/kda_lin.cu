@@ -245,7 +245,7 @@ kda_status_t kda_lin_chunk_fwd(const void* q, const void* k, const void* v, cons
         if ((bf16 ? launch_lin_bf16(a, true, s) : launch_lin_simt(a, true, s)) != cudaSuccess) return KDA_ERR_CUDA;
         const int elems = dk * dv;
         const unsigned bx = static_cast<unsigned>((static_cast<size_t>(H) * elems / 4 + 255) / 256);
-        const dim3 grid(bx, static_cast<unsigned>(std::min(l.max_bounds, 64)));
+        const dim3 grid(bx, std::min(static_cast<unsigned>(l.max_bounds), std::max(1u, 4u * kLinSms / bx)));
         if (launch_chained(lin_join_kernel, grid, dim3(256), s, a.head, a.multi, a.z, a.zdecay, H, elems) != cudaSuccess)
             return KDA_ERR_CUDA;
     }

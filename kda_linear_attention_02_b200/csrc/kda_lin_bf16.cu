@@ -48,8 +48,9 @@ struct Cfg {
     static constexpr uint32_t QB = BOUNDARY ? 0 : DK / 64 * HALF, KB = DK / 64 * HALF, VB = DV / 64 * HALF;
     static constexpr uint32_t STAGE = QB + KB + VB;
     static constexpr int NST = BOUNDARY ? 5 : (STAGE > 40960 ? 3 : 4);
-    // Decays outlive their chunk's tiles: the last to read those of chunk c, in writing o (the boundary pass: in
-    // taking Z), is done before the products of chunk c + 2 are, and those free the tiles of chunk c + 2 + NST.
+    // Decays outlive their chunk's tiles, and are written before the stage is free: when those of chunk c are, the
+    // products of chunk c - 1 - NST are known to be done, so that o of chunk c - 2 - NST has been written (and in the
+    // boundary pass Z of it taken).
     static constexpr int ND = NST + 2;
     static constexpr uint32_t PB = C * 128;                          // P: 64 rows of 64 bf16
     static constexpr uint32_t P0 = NST * STAGE, O0 = P0 + (BOUNDARY ? 0 : 2 * PB);
@@ -151,14 +152,29 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, float* r) {
         : "r"(taddr));
 }
 
-// mbar_wait in few instructions, since the roles' code together has to fit the SM's instruction caches (see the
-// kernel): polls that let the warp sleep for a while, bounded by their number; the caller records a wait that
+// mbar_wait in few instructions, since the roles' code together has to fit the SM's instruction cache: polls that
+// let the warp sleep for a while, bounded by their number (tenths of a second); the caller records a wait that
 // ran out.
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
-#pragma unroll 1
-    for (int i = 0; i < (1 << 22); ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    return false;
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+        "POLL:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 4194304;\n\t@q bra POLL;\n"
+        "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// One arrival for the warp, once all its lanes are here.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, bool yes = true) {
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 st;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(static_cast<uint32_t>(yes && (threadIdx.x & 31) == 0))
+        : "memory");
 }
 
 // 4 bytes global -> shared by an asynchronous copy, zero when not `valid` (nothing is read then)
@@ -173,6 +189,79 @@ __device__ __forceinline__ float exp_fast(float x) {
     return fmaf(e, r * 0.69314718f, e);
 }
 
+// One warp's walk over the log_alpha of a segment: the decays of its chunks, in order.  Lane i has tokens 2 i and
+// 2 i + 1 of a chunk, and fetches theirs three chunks ahead (a load takes longer than a chunk), to shared memory,
+// since moving a value on in registers would wait for its load.
+struct DecayWalk {
+    const float* la;
+    const float* any;      // a valid address for copies that read nothing
+    int la_t, n, left, lane;
+    float* ring;           // this lane's pair in the first of four slots of kChunk
+    float total;           // sum over the chunks so far
+
+    __device__ __forceinline__ void fetch(int c) {
+        const uint32_t at = smem_u32(ring + (c & 3) * kChunk);
+        cp_async4(at, left > 0 ? la : any, left > 0);
+        cp_async4(at + 4, left > 1 ? la + la_t : any, left > 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        la += kChunk * static_cast<size_t>(la_t);
+        left -= kChunk;
+    }
+    __device__ __forceinline__ void start(const LinArgs& a, const LinItem& it, int h, float* slots) {
+        lane = threadIdx.x & 31;
+        cp_async_wait_all();   // before the ring is filled anew
+        any = a.la;
+        la_t = a.la_t;
+        la = a.la + (static_cast<size_t>(it.t0) + 2 * lane) * la_t + h;
+        n = it.n;
+        left = n - 2 * lane;
+        ring = slots + 2 * lane;
+        total = 0.f;
+        if (n > 0)
+#pragma unroll 1
+            for (int c = 0; c < 3; ++c) fetch(c);
+    }
+    __device__ __forceinline__ void chunk(int c, Decays& d) {
+        fetch(c + 3);
+        asm volatile("cp.async.wait_group 3;" ::: "memory");
+        const float2 x = *reinterpret_cast<const float2*>(ring + (c & 3) * kChunk);
+        const bool in0 = c * kChunk + 2 * lane < n, in1 = c * kChunk + 2 * lane + 1 < n;
+        const float x0 = in0 ? fmaxf(x.x, kLinLogMin) : 0.f, x1 = in1 ? fmaxf(x.y, kLinLogMin) : 0.f;
+        // inclusive sums of the lanes' pairs, from the chunk's start and from its end
+        float f = x0 + x1, r = f;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float u = __shfl_up_sync(0xffffffffu, f, off), v = __shfl_down_sync(0xffffffffu, r, off);
+            if (lane >= off) f += u;
+            if (lane + off < 32) r += v;
+        }
+        float before = __shfl_up_sync(0xffffffffu, f, 1), after = __shfl_down_sync(0xffffffffu, r, 1);
+        if (lane == 0) before = 0.f;
+        if (lane == 31) after = 0.f;
+        const float sum = __shfl_sync(0xffffffffu, f, 31), gm = __shfl_sync(0xffffffffu, f, 15);
+        const float2 gt = make_float2(before + x0, f);
+        *reinterpret_cast<float2*>(&d.g2[2 * lane]) = make_float2(gt.x * kLog2e, gt.y * kLog2e);
+        *reinterpret_cast<float2*>(&d.eg[2 * lane]) = make_float2(exp_fast(gt.x), exp_fast(gt.y));
+        float w0 = exp_fast(after + x1), w1 = exp_fast(after);
+        uint32_t part[3];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            part[p] = pack_bf16x2(w0, w1);
+            w0 -= lo_f32(part[p]);
+            w1 -= hi_f32(part[p]);
+        }
+        d.w[lane] = make_uint4(part[0], part[1], part[2] ^ 0x80008000u, 0u);
+        if (lane < 16)
+            *reinterpret_cast<float2*>(&d.m[2 * lane]) =
+                make_float2(ex2_approx((gm - gt.x) * kLog2e), ex2_approx((gm - gt.y) * kLog2e));
+        if (lane == 0) {
+            d.g2m = gm * kLog2e;
+            d.eC = exp_fast(sum);
+        }
+        total += sum;
+    }
+};
+
 template <int DK, int DV, bool BOUNDARY>
 __global__ void __launch_bounds__(kThreads, 1)
 lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -182,7 +271,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ Decays decays[F::ND];
-    __shared__ __align__(8) float la_ring[4][C];
+    __shared__ __align__(8) float la_ring[4 * C];
     __shared__ __align__(8) uint64_t full[NST], empty[NST], sp_full, sp_free, p_ready[2], p_free[2], w_go[2], w_free[2], z_free[2],
         z_full[2], o_go, sb_free, o_full, done, job_full[2], job_free[2], w_sync, o_sync;
     __shared__ Job jobs[2];
@@ -211,7 +300,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         mbar_init(&done, 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&job_full[b], 1);
-            mbar_init(&job_free[b], 1 + kWWarps + kSWarps + (BOUNDARY ? 0 : kPWarps + kOWarps));
+            mbar_init(&job_free[b], 1 + kWWarps + kSWarps + kOWarps + (BOUNDARY ? 1 : kPWarps));
         }
         mbar_init(&w_sync, kWWarps);
         mbar_init(&o_sync, kOWarps);
@@ -237,14 +326,12 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         const Job& j = jobs[k & 1];
         it = j.it;
         h = j.h;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&job_free[k & 1]);
+        warp_arrive(&job_free[k & 1]);
         return h >= 0;
     };
     // Four warps meet (bounded, as all waits are; a named barrier would not be).
     auto meet = [&](uint64_t* bar, int& n) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
+        warp_arrive(bar);
         ok = ok && bar_wait(bar, n & 1);
         ++n;
     };
@@ -266,6 +353,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     return;
                 }
             };
+            DecayWalk walk;
             Job next;
             if (lane == 0) claim(true, next);
             int s = 0, ph = 1, g = 0;   // stage and its parity, chunks so far
@@ -279,79 +367,21 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 if (lane == 0) mbar_arrive(&job_full[k & 1]);
                 if (h < 0) break;
                 const int nch = (it.n + C - 1) / C, hq = h / (a.H / a.Hqk);
-                // log_alpha of this lane's tokens 2 lane and 2 lane + 1, three chunks ahead: a load takes longer than
-                // a chunk.  Copied to shared memory, since moving a value on in registers would wait for its load.
-                const float* la = a.la + (static_cast<size_t>(it.t0) + 2 * lane) * a.la_t + h;
-                const uint32_t la_at = smem_u32(&la_ring[0][2 * lane]);
-                int left = it.n - 2 * lane;   // tokens of the segment from the lane's first one on
-                auto fetch = [&](int c) {
-                    const uint32_t at = la_at + (c & 3) * static_cast<uint32_t>(sizeof(la_ring[0]));
-                    cp_async4(at, left > 0 ? la : a.la, left > 0);
-                    cp_async4(at + 4, left > 1 ? la + a.la_t : a.la, left > 1);
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    la += C * static_cast<size_t>(a.la_t);
-                    left -= C;
-                };
-                float total = 0.f;
-                if (nch > 0)
-#pragma unroll 1
-                    for (int c = 0; c < 3; ++c) fetch(c);
+                if (!BOUNDARY) walk.start(a, it, h, la_ring);
 #pragma unroll 1
                 for (int c = 0; c < nch; ++c, ++g) {
+                    // the decays ahead of the wait for the stage
+                    if (!BOUNDARY) walk.chunk(c, decays[g % F::ND]);
+                    // the tiles: halves of q, k and v lie one behind another in the stage, a lane issues each
                     if (!(ok = bar_wait(&empty[s], ph))) break;
-                    if (lane == 0) {
-                        uint8_t* sb = sm + s * F::STAGE;
-                        mbar_arrive_expect_tx(&full[s], F::STAGE);
-                        const int tok = it.t0 + c * C;
-#pragma unroll 1
-                        for (int b = 0; b < DK / 64; ++b) {
-                            if (!BOUNDARY) tma_load_2d(sb + b * F::HALF, &mq, hq * DK + 64 * b, tok, &full[s]);
-                            tma_load_2d(sb + F::QB + b * F::HALF, &mk, hq * DK + 64 * b, tok, &full[s]);
-                        }
-#pragma unroll 1
-                        for (int b = 0; b < DV / 64; ++b)
-                            tma_load_2d(sb + F::QB + F::KB + b * F::HALF, &mv, h * DV + 64 * b, tok, &full[s]);
-                    }
-                    fetch(c + 3);
-                    asm volatile("cp.async.wait_group 3;" ::: "memory");
-                    const float2 x = *reinterpret_cast<const float2*>(&la_ring[c & 3][2 * lane]);
-                    const bool in0 = c * C + 2 * lane < it.n, in1 = c * C + 2 * lane + 1 < it.n;
-                    const float x0 = in0 ? fmaxf(x.x, kLinLogMin) : 0.f, x1 = in1 ? fmaxf(x.y, kLinLogMin) : 0.f;
-                    // inclusive sums of the lanes' pairs, from the chunk's start and from its end
-                    float f = x0 + x1, r = f;
-#pragma unroll 1
-                    for (int off = 1; off < 32; off <<= 1) {
-                        const float u = __shfl_up_sync(0xffffffffu, f, off), v = __shfl_down_sync(0xffffffffu, r, off);
-                        if (lane >= off) f += u;
-                        if (lane + off < 32) r += v;
-                    }
-                    float before = __shfl_up_sync(0xffffffffu, f, 1), after = __shfl_down_sync(0xffffffffu, r, 1);
-                    if (lane == 0) before = 0.f;
-                    if (lane == 31) after = 0.f;
-                    const float sum = __shfl_sync(0xffffffffu, f, 31), gm = __shfl_sync(0xffffffffu, f, 15);
-                    Decays& d = decays[g % F::ND];
-                    const float2 gt = make_float2(before + x0, f);
-                    *reinterpret_cast<float2*>(&d.g2[2 * lane]) = make_float2(gt.x * kLog2e, gt.y * kLog2e);
-                    *reinterpret_cast<float2*>(&d.eg[2 * lane]) = make_float2(exp_fast(gt.x), exp_fast(gt.y));
-                    float w0 = exp_fast(after + x1), w1 = exp_fast(after);
-                    uint32_t part[3];
-#pragma unroll
-                    for (int p = 0; p < 3; ++p) {
-                        part[p] = pack_bf16x2(w0, w1);
-                        w0 -= lo_f32(part[p]);
-                        w1 -= hi_f32(part[p]);
-                    }
-                    d.w[lane] = make_uint4(part[0], part[1], part[2] ^ 0x80008000u, 0u);
-                    if (lane < 16)
-                        *reinterpret_cast<float2*>(&d.m[2 * lane]) =
-                            make_float2(ex2_approx((gm - gt.x) * kLog2e), ex2_approx((gm - gt.y) * kLog2e));
-                    if (lane == 0) {
-                        d.g2m = gm * kLog2e;
-                        d.eC = exp_fast(sum);
-                    }
-                    total += sum;
+                    if (lane == 0) mbar_arrive_expect_tx(&full[s], F::STAGE);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[s]);
+                    constexpr int NQ = F::QB / F::HALF, NK = NQ + DK / 64, NV = NK + DV / 64;
+                    if (lane < NV)
+                        tma_load_2d(sm + s * F::STAGE + lane * F::HALF, lane < NQ ? &mq : lane < NK ? &mk : &mv,
+                                    lane < NK ? hq * DK + 64 * (lane < NQ ? lane : lane - NQ) : h * DV + 64 * (lane - NK),
+                                    it.t0 + c * C, &full[s]);
+                    if (!BOUNDARY) warp_arrive(&full[s]);   // (written ahead of the barrier above)
                     if (++s == NST) {
                         s = 0;
                         ph ^= 1;
@@ -359,10 +389,9 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     // late, so that a CTA with a long pair does not sit on another
                     if (c == max(nch - 2, 0) && lane == 0) claim(false, next);
                 }
-                if (BOUNDARY && lane == 0) a.zdecay[static_cast<size_t>(it.z0 + it.seg) * a.H + h] = exp_fast(total);
                 if (nch == 0 && lane == 0) claim(false, next);
-                cp_async_wait_all();   // before the ring is filled anew
             }
+            cp_async_wait_all();
             // no copy stays in flight behind the CTA: wait (bounded, quietly) for the last fill of every stage
 #pragma unroll 1
             for (int c = g > NST ? g - NST : 0; c < g; ++c) bar_wait(&full[c % NST], (c / NST) & 1);
@@ -371,13 +400,15 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             constexpr uint32_t id_o = idesc_bf16(128, C), id_o2 = idesc_bf16(128, C, false, false, true),
                                id_z = idesc_bf16(128, DK, false, true), neg_a = 1u << 13;
             const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0), base = __shfl_sync(0xffffffffu, smem_u32(sm), 0);
-            // K = 16 slice i of a K-major tile of 64-channel halves, in descriptor units
-            auto slice = [](int i) { return static_cast<uint32_t>((i >> 2) * (F::HALF >> 4) + (i & 3) * 2); };
+            // K-major tiles: halves of 64 channels, 32 bytes (2 in a descriptor) for each 16
             auto scores = [&](int s) {
                 const uint32_t q = base + s * F::STAGE, k = q + F::QB;
                 const uint64_t qd = sdesc_k_sw128(q), kd = sdesc_k_sw128(k);
+#pragma unroll 1
+                for (uint32_t b = 0; b < DK / 64; ++b)
 #pragma unroll
-                for (int i = 0; i < DK / 16; ++i) mma_ss(tmu + F::SP, qd + slice(i), kd + slice(i), id_o, i > 0);
+                    for (uint32_t i = 0; i < 4; ++i)
+                        mma_ss(tmu + F::SP, qd + b * (F::HALF >> 4) + 2 * i, kd + b * (F::HALF >> 4) + 2 * i, id_o, b + i > 0);
                 mma_commit(&sp_full);
             };
             int s = 0, ph = 0, g = 0;   // stage and its parity, chunks so far
@@ -402,7 +433,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     const uint32_t zcol = tmu + F::Z + (g % F::NZ) * 128;
                     auto z_half = [&](int half) {
                         tc_fence_after();
-#pragma unroll 1
+#pragma unroll 2
                         for (int i = 0; i < 8; ++i) {   // part i / 2, tokens 32 half + 16 (i % 2) ..; odd parts are negated
                             const int sl = 2 * half + (i & 1);
                             mma_ts(zcol, tmu + F::W + 32 * (i >> 1) + 8 * sl, kd + sl * (2048 >> 4), id_z | ((i & 2) ? neg_a : 0u),
@@ -426,8 +457,11 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         if (!(ok = bar_wait(&o_go, g & 1))) break;
                         tc_fence_after();
                         const uint64_t qd = sdesc_k_sw128(q);
+#pragma unroll 1
+                        for (uint32_t b = 0; b < DK / 64; ++b)
 #pragma unroll
-                        for (int i = 0; i < DK / 16; ++i) mma_ts(tmu + F::O1, tmu + F::SB + 8 * i, qd + slice(i), id_o, i > 0);
+                            for (uint32_t i = 0; i < 4; ++i)
+                                mma_ts(tmu + F::O1, tmu + F::SB + 32 * b + 8 * i, qd + b * (F::HALF >> 4) + 2 * i, id_o, b + i > 0);
                         mma_commit(&sb_free);
                         if (!(ok = bar_wait(&p_ready[g & 1], (g >> 1) & 1))) break;
                         tc_fence_after();
@@ -444,9 +478,33 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             }
             mma_commit(&done);
             ok = bar_wait(&done, 0) && ok;   // no product stays in flight behind the CTA
+        } else if (BOUNDARY) {
+            // ---------------- decays, where a chunk takes less time than forming them and issuing its copies
+            if (w == 1) {
+                DecayWalk walk;
+                LinItem it;
+                int h, s = 0, ph = 1, g = 0;
+#pragma unroll 1
+                for (int job = 0; ok && next_job(job, it, h); ++job) {
+                    walk.start(a, it, h, la_ring);
+                    const int nch = (it.n + C - 1) / C;
+#pragma unroll 1
+                    for (int c = 0; c < nch; ++c, ++g) {
+                        if (!(ok = bar_wait(&empty[s], ph))) break;
+                        walk.chunk(c, decays[g % F::ND]);
+                        warp_arrive(&full[s]);
+                        if (++s == NST) {
+                            s = 0;
+                            ph ^= 1;
+                        }
+                    }
+                    if (lane == 0) a.zdecay[static_cast<size_t>(it.z0 + it.seg) * a.H + h] = exp_fast(walk.total);
+                }
+                cp_async_wait_all();
+            }
         } else {
             // ---------------- P: warp w has rows 32 w .. 32 w + 31; columns above the diagonal blocks stay zero
-            if (!BOUNDARY) {
+            {
                 const int row = 32 * w + lane;
                 uint8_t* p0 = sm + F::P0 + row * 128;
                 if (w == 0)
@@ -459,9 +517,6 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         *reinterpret_cast<uint4*>(p + (((j0 / 8 + i) ^ (row & 7)) << 4)) =
                             make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
                 };
-                uint32_t mask[16];   // of the diagonal block's pairs: columns up to the row's own
-#pragma unroll
-                for (int j = 0; j < 16; ++j) mask[j] = 2 * j + 1 <= lane ? 0xffffffffu : 2 * j <= lane ? 0x0000ffffu : 0u;
                 int s = 0, ph = 0, g = 0;
                 LinItem it;
                 int h;
@@ -493,27 +548,27 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         }
                         put(p, j0, u);
                     }
-                    float x[32];
-                    uint32_t u[16];
-                    tmem_ld32(at + 32 * w, x);
-                    tmem_wait_ld_regs<32>(x);
+#pragma unroll 1
+                    for (int j0 = 32 * w; j0 < 32 * w + 32; j0 += 16) {
+                        float x[16];
+                        uint32_t u[8];
+                        tmem_ld16(at + j0, x);
+                        tmem_wait_ld_regs<16>(x);
+                        const int k = row - j0;   // the row's own column: what lies behind it is cut off
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {   // what lies above the diagonal is cut off after the packing
-                        const float4 gj = *reinterpret_cast<const float4*>(&d.g2[32 * w + j]);
-                        u[j / 2] = mask[j / 2] & pack_bf16x2(x[j] * ex2_approx(gr - gj.x), x[j + 1] * ex2_approx(gr - gj.y));
-                        u[j / 2 + 1] =
-                            mask[j / 2 + 1] & pack_bf16x2(x[j + 2] * ex2_approx(gr - gj.z), x[j + 3] * ex2_approx(gr - gj.w));
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 gj = *reinterpret_cast<const float4*>(&d.g2[j0 + j]);
+                            u[j / 2] = pack_bf16x2(j <= k ? x[j] * ex2_approx(gr - gj.x) : 0.f,
+                                                   j + 1 <= k ? x[j + 1] * ex2_approx(gr - gj.y) : 0.f);
+                            u[j / 2 + 1] = pack_bf16x2(j + 2 <= k ? x[j + 2] * ex2_approx(gr - gj.z) : 0.f,
+                                                       j + 3 <= k ? x[j + 3] * ex2_approx(gr - gj.w) : 0.f);
+                        }
+                        put(p, j0, u);
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4*>(p + (((4 * w + i) ^ (row & 7)) << 4)) =
-                            make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
                     tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sp_free);
+                    warp_arrive(&sp_free);
                     fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_ready[g & 1]);
+                    warp_arrive(&p_ready[g & 1]);
                     if (++s == NST) {
                         s = 0;
                         ph ^= 1;
@@ -538,8 +593,11 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         int s = 0, ph = 0, g = 0, met = 0;
         LinItem it;
         int h;
-        if (w < 8) {
-            // ---------------- W
+        if (w < 8 || BOUNDARY) {
+            // ---------------- W: all tokens, or in the boundary pass, where there is no o to write, 32 for each four
+            // warps
+            const int from = BOUNDARY && w >= 8 ? 32 : 0, to = BOUNDARY ? from + 32 : C;
+            uint64_t* const sync = BOUNDARY && w >= 8 ? &o_sync : &w_sync;
 #pragma unroll 1
             for (int job = 0; ok && next_job(job, it, h); ++job)
 #pragma unroll 1
@@ -560,7 +618,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                             *reinterpret_cast<uint4*>(vt + b * F::HALF + x) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
-                    meet(&w_sync, met);
+                    meet(sync, met);
                 }
                 const Decays& d = decays[g % F::ND];
                 uint32_t v[2][4];
@@ -569,47 +627,48 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     ldsm_x4_trans(smem_u32(vt) + row + half * 128, v[0]);
                     ldsm_x4_trans(smem_u32(vt) + row + half * 128 + 16 * 128, v[1]);
                 };
-                if (mine) load_v(row0, 0);
+                if (mine) load_v(row0, from);
 #pragma unroll 1
-                for (int half = 0; half < C; half += 32) {
+                for (int half = from; half < to; half += 32) {
 #pragma unroll
                     for (int b = 0; b < 4; ++b) wb[b] = d.w[half / 2 + 4 * b + (lane & 3)];
-#pragma unroll 1
-                    for (int lh = 0; lh < 2; ++lh) {   // 16 channels, 32 tokens
-                        uint32_t u[4][8];
-                        if (mine) {
+                    uint32_t u[2][4][8];   // 32 tokens, 16 channels each
+                    if (mine) {
+#pragma unroll
+                        for (int lh = 0; lh < 2; ++lh) {
 #pragma unroll
                             for (int r = 0; r < 8; ++r) {   // block r / 2, channels 8 (r % 2) + lane / 4 of the sixteen
                                 const uint32_t x = v[r >> 2][r & 3];
                                 const uint4 w4 = wb[r >> 1];
-                                u[0][r] = fma_bf16x2(x, w4.x, 0x80008000u);
-                                u[1][r] = fma_bf16x2(x, w4.x ^ 0x80008000u, u[0][r]);
-                                u[2][r] = fma_bf16x2(x, w4.y, 0x80008000u);
-                                u[3][r] = fma_bf16x2(x, w4.z, fma_bf16x2(x, w4.y ^ 0x80008000u, u[2][r]));
+                                u[lh][0][r] = fma_bf16x2(x, w4.x, 0x80008000u);
+                                u[lh][1][r] = fma_bf16x2(x, w4.x ^ 0x80008000u, u[lh][0][r]);
+                                u[lh][2][r] = fma_bf16x2(x, w4.y, 0x80008000u);
+                                u[lh][3][r] = fma_bf16x2(x, w4.z, fma_bf16x2(x, w4.y ^ 0x80008000u, u[lh][2][r]));
                             }
                             if (lh == 0) load_v(row1, half);
-                            else if (half == 0) load_v(row0, 32);
+                            else if (half + 32 < to) load_v(row0, half + 32);
                         }
-                        if (lh == 0 && g > 0) wait(&w_free[half >> 5], (g - 1) & 1);
-                        if (mine && ok) {
-                            tc_fence_after();
+                    }
+                    if (g > 0) wait(&w_free[half >> 5], (g - 1) & 1);
+                    if (mine && ok) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int lh = 0; lh < 2; ++lh)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 tmem_st_16x128b_x4(tm + lanes + (static_cast<uint32_t>(16 * lh) << 16) + F::W + 32 * k + half / 2,
-                                                   u[k]);
-                        }
+                                                   u[lh][k]);
                     }
                     if (mine && ok) tmem_wait_st();
                     tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0 && ok) mbar_arrive(&w_go[half >> 5]);
+                    warp_arrive(&w_go[half >> 5], ok);
                 }
                 if (++s == NST) {
                     s = 0;
                     ph ^= 1;
                 }
             }
-        } else if (!BOUNDARY) {
+        } else {
             // ---------------- o
             // Leave for o of chunk c is given with the chunk's decays in sight: a stage is filled anew as soon as its
             // products are done, so nobody may look for a filling after it has let those go ahead.
@@ -619,8 +678,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     s = 0;
                     ph ^= 1;
                 }
-                __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(&o_go);
+                warp_arrive(&o_go, ok);
             };
 #pragma unroll 1
             for (int job = 0; ok && next_job(job, it, h); ++job) {
@@ -648,6 +706,10 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         for (int b = 0; b < 4; ++b) e[b] = *reinterpret_cast<const float2*>(&d.eg[half + 8 * b + 2 * (lane & 3)]);
                         tmem_wait_ld_regs<16>(x);
                         tmem_wait_ld_regs<16>(y);
+                        if (u4 == 3) {   // O1 and O2 have been read
+                            tc_fence_before();
+                            if (left > C) leave();
+                        }
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             uint32_t u[4];
@@ -660,10 +722,10 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                             stsm_x4_trans(smem_u32(ob) + (lh ? row1 : row0) + (half + 16 * i) * 128, u);
                         }
                     }
-                    tc_fence_before();
+                } else if (left > C) {
+                    leave();
                 }
                 fence_proxy_async_smem();
-                if (left > C) leave();
                 meet(&o_sync, met);
                 if (left >= C) {
                     if (tg == 0 && ok) {
@@ -703,8 +765,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 tmem_wait_st();
                 tc_fence_before();
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&o_go);
+            warp_arrive(&o_go);
         };
         int s = 0, ph = 0, g = 0;
         LinItem it;
@@ -721,62 +782,65 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             if (BOUNDARY) end = a.z + (static_cast<size_t>(it.z0 + it.seg) * a.H + h) * DK * DV;
             else if (a.final_state && it.seg + 1 == it.n_seg)
                 end = a.final_state + (static_cast<size_t>(it.seq) * a.H + h) * DK * DV;
-            if (it.n == 0) {   // no tokens: the state stays as it was
-                if (end && mine)
-#pragma unroll 1
-                    for (int i = 0; i < DK; ++i) end[i * DV + ch] = start ? start[i * DV + ch] : 0.f;
-                continue;
-            }
 #pragma unroll
             for (int i = 0; i < DK; ++i) S[i] = start && mine ? start[i * DV + ch] : 0.f;
-            // tokens to the next checkpoint, and its place
-            int to_ck = 0x7fffffff, ck = 0;
+            // tokens to the next checkpoint, its place, and how many places the table has from there
+            int to_ck = 0, ck_room = 0;
+            float* ck = nullptr;
             if (!BOUNDARY && a.ckpt_stride) {
+                const int first = a.ckpt_cu[it.seq] + it.pos / a.ckpt_stride;
                 to_ck = a.ckpt_stride - it.pos % a.ckpt_stride;
-                ck = a.ckpt_cu[it.seq] + it.pos / a.ckpt_stride;
+                ck_room = first >= 0 ? a.ckpt_cu[it.seq + 1] - first : 0;
+                ck = a.checkpoints + (static_cast<long long>(first) * a.H + h) * (DK * DV);
             }
+            int left = it.n;   // without tokens the state stays as it was
 #pragma unroll 1
-            for (int left = it.n; left > 0; left -= C, ++g) {
-                if (!(ok = bar_wait(&full[s], ph))) break;   // before Sb lets the chunk's products go ahead (see `leave`)
-                const float eC = decays[g % F::ND].eC;
-                if (BOUNDARY) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&empty[s]);
-                } else {
-                    if (g > 0 && !(ok = bar_wait(&sb_free, (g - 1) & 1))) break;   // the copy before has been read
-                    tc_fence_after();
-                    publish();
-                }
-                if (!(ok = bar_wait(&z_full[g & 1], (g >> 1) & 1))) break;
-                if (mine) {
-                    tc_fence_after();
-#pragma unroll
-                    for (int b = 0; b < DK; b += 32) {
-                        float z[32];
-                        tmem_ld32(tm + lanes + F::Z + (g % F::NZ) * 128 + b, z);
-                        tmem_wait_ld_regs<32>(z);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) S[b + i] = fmaf(eC, S[b + i], z[i]);
+            do {
+                float* dst = nullptr;
+                if (left > 0) {
+                    if (!(ok = bar_wait(&full[s], ph))) break;   // before Sb lets the chunk's products go ahead (see `leave`)
+                    const float eC = decays[g % F::ND].eC;
+                    if (BOUNDARY) {
+                        warp_arrive(&empty[s]);
+                    } else {
+                        if (g > 0 && !(ok = bar_wait(&sb_free, (g - 1) & 1))) break;   // the copy before has been read
+                        tc_fence_after();
+                        publish();
                     }
-                    tc_fence_before();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&z_free[g % F::NZ]);
-                if (++s == NST) {
-                    s = 0;
-                    ph ^= 1;
+                    if (!(ok = bar_wait(&z_full[g & 1], (g >> 1) & 1))) break;
+                    if (mine) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int b = 0; b < DK; b += 32) {
+                            float z[32];
+                            tmem_ld32(tm + lanes + F::Z + (g % F::NZ) * 128 + b, z);
+                            tmem_wait_ld_regs<32>(z);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                const float2 y = __ffma2_rn(make_float2(eC, eC), make_float2(S[b + i], S[b + i + 1]),
+                                                            make_float2(z[i], z[i + 1]));
+                                S[b + i] = y.x;
+                                S[b + i + 1] = y.y;
+                            }
+                        }
+                        tc_fence_before();
+                    }
+                    warp_arrive(&z_free[g % F::NZ]);
+                    if (++s == NST) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                    ++g;
+                    to_ck -= C;
+                    if (!BOUNDARY && to_ck == 0 && left >= C) {
+                        to_ck = a.ckpt_stride;
+                        if (ck_room > 0) dst = ck;
+                        else if (lane == 0) set_status(a.status, KDA_ERR_DEVICE_INPUT);
+                        --ck_room;
+                        ck += static_cast<size_t>(a.H) * (DK * DV);
+                    }
                 }
                 // a checkpoint, and the state at the segment's end
-                float* dst = nullptr;
-                to_ck -= C;
-                if (!BOUNDARY && to_ck == 0 && left >= C) {
-                    to_ck = a.ckpt_stride;
-                    if (ck >= 0 && ck < a.ckpt_cu[it.seq + 1])
-                        dst = a.checkpoints + (static_cast<size_t>(ck) * a.H + h) * DK * DV;
-                    else if (lane == 0)
-                        set_status(a.status, KDA_ERR_DEVICE_INPUT);
-                    ++ck;
-                }
                 float* const last = left <= C ? end : nullptr;
                 if (mine && (dst || last)) {
 #pragma unroll 1
@@ -787,7 +851,8 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                             for (int i = 0; i < DK; ++i) p[i * DV + ch] = S[i];
                     }
                 }
-            }
+                left -= C;
+            } while (left > 0);
         }
     }
     if (!ok && lane == 0) set_status(a.status, KDA_ERR_TIMEOUT);
