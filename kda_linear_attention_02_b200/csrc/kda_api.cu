@@ -3,6 +3,7 @@
 // the arithmetic of the operator lives in kda_decode.cu, kda_compose.cu, kda_chunk_f32.cu and
 // kda_chunk_bf16.cu.
 #include <algorithm>
+#include <atomic>
 
 #include "kda_device.cuh"
 #include "kda_internal.h"
@@ -139,10 +140,16 @@ kda_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_E
 
 }  // namespace
 
-// Device address of the current device's status word.
+// Device address of the current device's status word (looked up once per device).
 int* kda::status_ptr() {
+    static std::atomic<int*> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+    if (dev >= 0 && dev < 64)
+        if (int* p = known[dev].load(std::memory_order_relaxed)) return p;
     int* p = nullptr;
     if (cudaGetSymbolAddress(reinterpret_cast<void**>(&p), g_status) != cudaSuccess) return nullptr;
+    if (dev >= 0 && dev < 64) known[dev].store(p, std::memory_order_relaxed);
     return p;
 }
 

@@ -147,7 +147,7 @@ struct SegRule {
 };
 SegRule segment_rule(int64_t total_tokens, int H, int dv, bool bf16) {
     // fp32: a CTA has 32 columns of a state, and walks about five times as slowly
-    const int64_t per_token = bf16 ? H : static_cast<int64_t>(H) * (dv / 32), least = bf16 ? 512 : 128;
+    const int64_t per_token = bf16 ? H : static_cast<int64_t>(H) * (dv / 32), least = bf16 ? 512 : 64;
     const int64_t share = (total_tokens * per_token + kLinSms - 1) / kLinSms;
     auto chunks = [](int64_t tokens) { return (tokens + kChunk - 1) / kChunk * kChunk; };
     SegRule r{};
@@ -238,18 +238,20 @@ kda_status_t kda_lin_chunk_fwd(const void* q, const void* k, const void* v, cons
     if (!a.status) return KDA_ERR_CUDA;
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    LinMaps maps;
+    if (bf16 && !make_lin_maps(a, maps)) return KDA_ERR_CUDA;
     if (launch_chained(lin_index_kernel, dim3(1), dim3(1024), s, cu_seqlens, n_seqs, static_cast<int>(total_tokens),
                        l.seg.whole, l.seg.len, a.head, a.items, a.multi, a.status) != cudaSuccess)
         return KDA_ERR_CUDA;
     if (l.max_bounds > 0) {
-        if ((bf16 ? launch_lin_bf16(a, true, s) : launch_lin_simt(a, true, s)) != cudaSuccess) return KDA_ERR_CUDA;
+        if ((bf16 ? launch_lin_bf16(a, maps, true, s) : launch_lin_simt(a, true, s)) != cudaSuccess) return KDA_ERR_CUDA;
         const int elems = dk * dv;
         const unsigned bx = static_cast<unsigned>((static_cast<size_t>(H) * elems / 4 + 255) / 256);
         const dim3 grid(bx, std::min(static_cast<unsigned>(l.max_bounds), std::max(1u, 4u * kLinSms / bx)));
         if (launch_chained(lin_join_kernel, grid, dim3(256), s, a.head, a.multi, a.z, a.zdecay, H, elems) != cudaSuccess)
             return KDA_ERR_CUDA;
     }
-    return (bf16 ? launch_lin_bf16(a, false, s) : launch_lin_simt(a, false, s)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return (bf16 ? launch_lin_bf16(a, maps, false, s) : launch_lin_simt(a, false, s)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 kda_status_t kda_lin_recurrent_step(float* state, int64_t n_states, const int32_t* slots, int slot_stride,

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kda_internal.h"
 
 namespace kda {
@@ -64,10 +66,31 @@ struct LinArgs {
     int* status;
 };
 
+// Raises a kernel's dynamic shared memory limit, once per device (one static per kernel).
+struct SmemLimit {
+    std::atomic<unsigned long long> done{0};
+    cudaError_t raise(const void* kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+        if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+};
+
+// Tensor maps of q, k, v and o for the bf16 kernel, made once per call.
+struct LinMaps {
+    CUtensorMap q, k, v, o;
+};
+bool make_lin_maps(const LinArgs& a, LinMaps& m);
+
 // One pass over all segments (kda_lin_simt.cu: fp32 on the fp32 units; kda_lin_bf16.cu: bf16 on the tensor cores).
 // boundary_pass: only the segments with a successor, only their end states, into z and zdecay.
 cudaError_t launch_lin_simt(const LinArgs& a, bool boundary_pass, cudaStream_t s);
-cudaError_t launch_lin_bf16(const LinArgs& a, bool boundary_pass, cudaStream_t s);
+cudaError_t launch_lin_bf16(const LinArgs& a, const LinMaps& m, bool boundary_pass, cudaStream_t s);
 
 // Decode step (kda_lin_step.cu).
 cudaError_t launch_lin_step(float* state, int64_t n_states, const int32_t* slots, int slot_stride, const void* q,

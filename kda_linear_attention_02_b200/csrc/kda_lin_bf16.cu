@@ -874,21 +874,11 @@ bool make_map(CUtensorMap* m, const void* base, long long cols, long long T) {
 }
 
 template <int DK, int DV, bool BOUNDARY>
-cudaError_t launch(const LinArgs& a, cudaStream_t s) {
+cudaError_t launch(const LinArgs& a, const LinMaps& m, cudaStream_t s) {
     using F = Cfg<DK, DV, BOUNDARY>;
-    CUtensorMap mq, mk, mv, mo;
-    memset(&mq, 0, sizeof(mq));
-    memset(&mk, 0, sizeof(mk));
-    memset(&mv, 0, sizeof(mv));
-    memset(&mo, 0, sizeof(mo));
-    if (a.total_tokens > 0) {   // without tokens no tile is loaded or stored
-        const long long cq = static_cast<long long>(a.Hqk) * DK, cv = static_cast<long long>(a.H) * DV;
-        if (!make_map(&mq, a.q, cq, a.total_tokens) || !make_map(&mk, a.k, cq, a.total_tokens) ||
-            !make_map(&mv, a.v, cv, a.total_tokens) || !make_map(&mo, a.o, cv, a.total_tokens))
-            return cudaErrorInvalidValue;
-    }
     const int smem = static_cast<int>(F::BYTES) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(lin_bf16_kernel<DK, DV, BOUNDARY>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(reinterpret_cast<const void*>(&lin_bf16_kernel<DK, DV, BOUNDARY>), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     const long long jobs = static_cast<long long>(BOUNDARY ? a.max_bounds : a.max_items) * a.H;
@@ -901,19 +891,27 @@ cudaError_t launch(const LinArgs& a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lin_bf16_kernel<DK, DV, BOUNDARY>, a, mq, mk, mv, mo);
+    return cudaLaunchKernelEx(&cfg, lin_bf16_kernel<DK, DV, BOUNDARY>, a, m.q, m.k, m.v, m.o);
 }
 
 template <int DK, int DV>
-cudaError_t launch_b(const LinArgs& a, bool boundary_pass, cudaStream_t s) {
-    return boundary_pass ? launch<DK, DV, true>(a, s) : launch<DK, DV, false>(a, s);
+cudaError_t launch_b(const LinArgs& a, const LinMaps& m, bool boundary_pass, cudaStream_t s) {
+    return boundary_pass ? launch<DK, DV, true>(a, m, s) : launch<DK, DV, false>(a, m, s);
 }
 
 }  // namespace
 
-cudaError_t launch_lin_bf16(const LinArgs& a, bool boundary_pass, cudaStream_t s) {
-    if (a.dk == 64) return a.dv == 64 ? launch_b<64, 64>(a, boundary_pass, s) : launch_b<64, 128>(a, boundary_pass, s);
-    return a.dv == 64 ? launch_b<128, 64>(a, boundary_pass, s) : launch_b<128, 128>(a, boundary_pass, s);
+bool make_lin_maps(const LinArgs& a, LinMaps& m) {
+    memset(&m, 0, sizeof(m));
+    if (a.total_tokens == 0) return true;   // without tokens no tile is loaded or stored
+    const long long cq = static_cast<long long>(a.Hqk) * a.dk, cv = static_cast<long long>(a.H) * a.dv;
+    return make_map(&m.q, a.q, cq, a.total_tokens) && make_map(&m.k, a.k, cq, a.total_tokens) &&
+           make_map(&m.v, a.v, cv, a.total_tokens) && make_map(&m.o, a.o, cv, a.total_tokens);
+}
+
+cudaError_t launch_lin_bf16(const LinArgs& a, const LinMaps& m, bool boundary_pass, cudaStream_t s) {
+    if (a.dk == 64) return a.dv == 64 ? launch_b<64, 64>(a, m, boundary_pass, s) : launch_b<64, 128>(a, m, boundary_pass, s);
+    return a.dv == 64 ? launch_b<128, 64>(a, m, boundary_pass, s) : launch_b<128, 128>(a, m, boundary_pass, s);
 }
 
 }  // namespace kda

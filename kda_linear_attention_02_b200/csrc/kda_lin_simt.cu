@@ -283,7 +283,8 @@ __global__ void __launch_bounds__(kNt + 32) lin_simt_kernel(const LinArgs a) {
 template <int DK, bool BOUNDARY>
 cudaError_t launch(const LinArgs& a, cudaStream_t s) {
     constexpr int smem = sizeof(SimtSmem<DK>);
-    cudaError_t e = cudaFuncSetAttribute(lin_simt_kernel<DK, BOUNDARY>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(reinterpret_cast<const void*>(&lin_simt_kernel<DK, BOUNDARY>), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.max_items * a.H), a.dv / kDvs);
