@@ -177,6 +177,10 @@ __device__ __forceinline__ void named_bar_arrive(int id, int count) {
 // completed and its memory is visible (a no-op for an ordinary launch).
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lets the next kernel of the stream, launched with programmatic serialization, take its place on the SMs once
+// every block of this one has started; it still waits for this one's end before it touches memory.
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }

@@ -7,10 +7,27 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace kda {
 
 // The driver's tensor-map encoder (looked up once; nullptr when the driver lacks it) (kda_chunk_bf16.cu).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+// Raises a kernel's dynamic shared memory limit, once per device (one static per kernel).
+struct SmemLimit {
+    std::atomic<unsigned long long> done{0};
+    cudaError_t raise(const void* kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+        if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+};
 
 // Device address of the current device's status word, or null (kda_api.cu).
 int* status_ptr();

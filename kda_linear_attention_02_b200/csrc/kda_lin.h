@@ -4,8 +4,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "kda_internal.h"
 
 namespace kda {
@@ -15,10 +13,6 @@ namespace kda {
 constexpr float kLinLogMin = -120.f;
 
 constexpr int kLinSms = 148;   // SMs of a B200
-
-// Lets the next kernel of the stream, launched with programmatic serialization, take its place on the SMs once
-// every block of this one has started; it still waits for this one's end before it touches memory.
-__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // One segment of a sequence: what one CTA (of each head and slice) walks through, chunk by chunk.
 struct __align__(16) LinItem {
@@ -64,21 +58,6 @@ struct LinArgs {
     float* zdecay;               // [boundaries, H]
     int max_items, max_bounds;   // bounds the host knows
     int* status;
-};
-
-// Raises a kernel's dynamic shared memory limit, once per device (one static per kernel).
-struct SmemLimit {
-    std::atomic<unsigned long long> done{0};
-    cudaError_t raise(const void* kernel, int bytes) {
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
-        if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-        return e;
-    }
 };
 
 // Tensor maps of q, k, v and o for the bf16 kernel, made once per call.

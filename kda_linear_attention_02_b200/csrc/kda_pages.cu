@@ -73,6 +73,7 @@ __device__ __forceinline__ int hash_find(const int* key, int page) {
 
 __global__ void __launch_bounds__(kNt) pages_copy_kernel(const CopyArgs a) {
     __shared__ int s_d[kMaxGroup], s_s[kMaxGroup], key[kHash], writes[kHash], reads[kHash];
+    grid_launch_dependents();
     grid_dependency_wait();
     const int t = threadIdx.x, i0 = blockIdx.x / a.slices * a.group, slice = blockIdx.x % a.slices;
     const int m = min(a.group, a.n - i0);
@@ -161,6 +162,7 @@ __device__ __forceinline__ void carry_out(char* pool, int n_planes, int n_pages,
 __global__ void __launch_bounds__(kNt) pages_move_kernel(char* pool, int n_planes, int n_pages, size_t page_bytes,
                                                          const PlanHead* __restrict__ head,
                                                          const int2* __restrict__ moves, bool zero) {
+    grid_launch_dependents();
     grid_dependency_wait();
     carry_out(pool, n_planes, n_pages, page_bytes, moves, head->n_moves, zero);
 }
@@ -207,8 +209,15 @@ __global__ void __launch_bounds__(1024) pages_fork_plan_kernel(int32_t* refs, in
                                                                ForkEntry* entries, int2* moves, int* status) {
     extern __shared__ uint32_t opened[];
     __shared__ int warp_sums[32];
+    __shared__ ForkEntry near_entries[1024];   // the entries of a call that has no more
+    grid_launch_dependents();
     grid_dependency_wait();
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    if (n <= 1024) entries = near_entries;
+    // references of the first pages, which are looked at last: the block's steps each wait for a load
+    int ahead[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) ahead[u] = 4 * t + u < n_pages ? refs[4 * t + u] : 1;
     for (int i = t; i < (n_rows + 31) / 32; i += 1024) opened[i] = 0u;
     __syncthreads();
     bool bad = false;
@@ -258,7 +267,7 @@ __global__ void __launch_bounds__(1024) pages_fork_plan_kernel(int32_t* refs, in
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int p = base + 4 * t + u;
-            f[u] = p < n_pages && refs[p] == 0;
+            f[u] = base == 0 ? ahead[u] == 0 : p < n_pages && refs[p] == 0;
             k += f[u];
         }
         int total, at = found + block_scan(k, warp_sums, total);
@@ -305,6 +314,7 @@ __global__ void __launch_bounds__(1024) pages_fork_plan_kernel(int32_t* refs, in
 __global__ void __launch_bounds__(kNt) pages_free_kernel(int32_t* refs, int n_pages, const int32_t* __restrict__ table,
                                                          int32_t* counts, int n_rows, int max_pages,
                                                          const int32_t* __restrict__ rows, int n, int* status) {
+    grid_launch_dependents();
     grid_dependency_wait();
     const int i = blockIdx.x * (kNt / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (i >= n) return;
@@ -335,6 +345,7 @@ __global__ void __launch_bounds__(kNt) pages_free_kernel(int32_t* refs, int n_pa
 __global__ void __launch_bounds__(1024) pages_compact_plan_kernel(int32_t* refs, int n_pages, int32_t* __restrict__ remap,
                                                                   int32_t* n_live_out, PlanHead* head, int2* moves) {
     __shared__ int warp_sums[32];
+    grid_launch_dependents();
     grid_dependency_wait();
     const int t = threadIdx.x;
     int mine = 0, n_live;
@@ -397,6 +408,7 @@ __global__ void __launch_bounds__(kNt) pages_compact_kernel(char* pool, int n_pl
                                                             const int2* __restrict__ moves, int32_t* __restrict__ table,
                                                             const int32_t* __restrict__ counts, int n_rows, int max_pages,
                                                             const int32_t* __restrict__ remap, int* status) {
+    grid_launch_dependents();
     grid_dependency_wait();
     const long long entries = static_cast<long long>(n_rows) * max_pages;
     bool bad = false;
@@ -521,8 +533,8 @@ kda_status_t kda_pages_fork(void* pool, int n_planes, int n_pages, size_t page_b
     if (!st) return KDA_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const size_t smem = (static_cast<size_t>(n_rows) + 31) / 32 * 4;
-    if (smem > 40960 && cudaFuncSetAttribute(pages_fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kMaxRows / 8) != cudaSuccess)
+    static SmemLimit limit;
+    if (smem > 24576 && limit.raise(reinterpret_cast<const void*>(&pages_fork_plan_kernel), kMaxRows / 8) != cudaSuccess)
         return KDA_ERR_CUDA;
     if (launch_chained(pages_fork_plan_kernel, 1, 1024, smem, s, refs, n_pages, table, counts, n_rows, max_pages, parents,
                        children, n_shared, n_fresh, n, head, entries, moves, st) != cudaSuccess)

@@ -272,6 +272,21 @@ def test_corrupt_tables_are_reported_and_stay_in_bounds():
     assert status() == -7
 
 
+@pytest.mark.parametrize("n_rows", [150_000, 260_000, 400_000, 1 << 20])
+def test_fork_with_many_rows(n_rows):
+    # a bit for each row in the planning block's shared memory: below and above the default limit, and the most
+    pool = rand_pages(1, 4000, 4, seed=11)
+    c = Cache(pool, n_rows, 2)
+    rows = list(range(0, n_rows, n_rows // 1500))[:1500] + [n_rows - 1]      # more entries than one round takes
+    c.fork([-1] * len(rows), rows, fresh=[1] * len(rows))
+    assert status() == 0
+    assert c.table[rows, 0].tolist() == list(range(len(rows))) and int(c.counts.sum()) == len(rows)
+    c.fork([n_rows - 1, -1], [1, n_rows - 1], fresh=[0, 1])                  # opened and continued at once
+    assert status() == -7 and int(c.counts.sum()) == len(rows)
+    c.fork([n_rows - 1], [1], shared=[1])
+    assert status() == 0 and c.table[1, 0] == c.table[n_rows - 1, 0]
+
+
 def test_compact_of_full_and_empty_caches():
     for fresh in ([3, 3, 3, 3], [0, 0, 0, 0]):
         pool = rand_pages(2, 12, 4, seed=9)
