@@ -102,7 +102,8 @@ __global__ void __launch_bounds__(256) lin_join_kernel(const LinHead* __restrict
                                                        int elems) {
     grid_launch_dependents();
     grid_dependency_wait();
-    const int e4 = (blockIdx.x * 256 + threadIdx.x) * 4, h = e4 / elems;
+    const long long e4 = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 4;
+    const int h = static_cast<int>(e4 / elems);
     if (h >= H) return;
     for (int m = blockIdx.y; m < head->n_multi; m += gridDim.y) {
         const int z0 = multi[m].x, nb = multi[m].y - 1;
@@ -217,6 +218,10 @@ kda_status_t kda_lin_chunk_fwd(const void* q, const void* k, const void* v, cons
     if ((log_alpha && !aligned(log_alpha, 4)) || !aligned(cu_seqlens, 4) || (ckpt_cu && !aligned(ckpt_cu, 4)))
         return KDA_ERR_ALIGN;
     if (!aligned(workspace, 256)) return KDA_ERR_ALIGN;
+    // a later segment of a sequence may be done, and the final state written, before an earlier one starts
+    const uintptr_t st_bytes = static_cast<uintptr_t>(n_seqs) * H * dk * dv * sizeof(float);
+    const uintptr_t s0 = reinterpret_cast<uintptr_t>(initial_state), s1 = reinterpret_cast<uintptr_t>(final_state);
+    if (s0 && s1 && s0 < s1 + st_bytes && s1 < s0 + st_bytes) return KDA_ERR_ARG;
     const bool bf16 = dtype == KDA_BF16;
     const LinLayout l = layout(total_tokens, n_seqs, H, dk, dv, bf16);
     if (ws_bytes < l.total) return KDA_ERR_WORKSPACE;

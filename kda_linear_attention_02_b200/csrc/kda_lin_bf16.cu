@@ -153,14 +153,14 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, float* r) {
 }
 
 // mbar_wait in few instructions, since the roles' code together has to fit the SM's instruction cache: polls that
-// let the warp sleep for a while, bounded by their number (tenths of a second); the caller records a wait that
-// ran out.
+// let the warp sleep (two microseconds each, measured), bounded by their number, so about two seconds; the caller
+// records a wait that ran out.
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
         "POLL:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
-        "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 4194304;\n\t@q bra POLL;\n"
+        "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 1048576;\n\t@q bra POLL;\n"
         "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(smem_u32(bar)), "r"(parity)

@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(1024) pages_fork_plan_kernel(int32_t* refs, in
             if (ok) {
                 e.have = p >= 0 ? counts[p] : 0;
                 e.keep = p == c ? e.have : p >= 0 && n_shared ? n_shared[i] : 0;
-                ok = e.have >= 0 && e.have <= max_pages && e.keep >= 0 && e.keep <= e.have && e.have + fresh <= max_pages &&
+                ok = e.have >= 0 && e.have <= max_pages && e.keep >= 0 && e.keep <= e.have && fresh <= max_pages - e.have &&
                      (p == c || counts[c] == 0) && !(atomicOr(&opened[c >> 5], 1u << (c & 31)) >> (c & 31) & 1u);
             }
             e.count = ok ? e.have - e.keep + fresh : 0;

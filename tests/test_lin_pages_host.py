@@ -33,7 +33,8 @@ def chunk(lib, **over):
     (dict(dt=2), ARG), (dict(dt=7), ARG), (dict(q=None), ARG), (dict(k=None), ARG), (dict(v=None), ARG), (dict(la=None), ARG),
     (dict(o=None), ARG), (dict(cu=None), ARG), (dict(ws=None), ARG), (dict(dk=96), UNSUPPORTED), (dict(dv=256), UNSUPPORTED),
     (dict(q=0x1008), ALIGN), (dict(o=0x7002), ALIGN), (dict(s0=0x8004), ALIGN), (dict(fs=0x8004), ALIGN), (dict(la=0x4002), ALIGN),
-    (dict(cu=0x6001), ALIGN), (dict(ws=0x10080), ALIGN), (dict(wsb=64), WORKSPACE), (dict(n=0), ARG)])
+    (dict(cu=0x6001), ALIGN), (dict(ws=0x10080), ALIGN), (dict(wsb=64), WORKSPACE), (dict(n=0), ARG),
+    (dict(s0=0x100000, fs=0x100000), ARG), (dict(s0=0x100000, fs=0x100000 + 2 * 4 * 128 * 128 * 4 - 16), ARG)])
 def test_chunk_refusals(lib, over, want):
     assert chunk(lib, **over) == want
 
