@@ -734,6 +734,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         bulk_commit();
                     }
                 } else {   // the rows behind the sequence are not this one's to write
+                    if (tg == 0) bulk_commit();   // an empty group: the wait above counts one for every chunk
                     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + (static_cast<size_t>(tok) * a.H + h) * DV;
 #pragma unroll 1
                     for (int i = tg; ok && i < left * (DV / 8); i += 128) {
