@@ -53,7 +53,7 @@ struct Cfg {
     // boundary pass Z of it taken).
     static constexpr int ND = NST + 2;
     static constexpr uint32_t PB = C * 128;                          // P: 64 rows of 64 bf16
-    static constexpr uint32_t P0 = NST * STAGE, O0 = P0 + (BOUNDARY ? 0 : 2 * PB);
+    static constexpr uint32_t P0 = NST * STAGE, O0 = P0 + (BOUNDARY ? 0 : 4 * PB);   // two places of two parts
     // the A operands of 128 rows read past 64-row tiles (their results are not used): the tiles behind exist
     static constexpr uint32_t BYTES = O0 + (BOUNDARY ? HALF : 2 * VB);
     // tensor memory columns
@@ -465,9 +465,12 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         mma_commit(&sb_free);
                         if (!(ok = bar_wait(&p_ready[g & 1], (g >> 1) & 1))) break;
                         tc_fence_after();
-                        const uint64_t vd = sdesc_mn_sw128(v, F::HALF), pd = sdesc_k_sw128(base + F::P0 + (g & 1) * F::PB);
+                        const uint64_t vd = sdesc_mn_sw128(v, F::HALF), pd = sdesc_k_sw128(base + F::P0 + (g & 1) * 2 * F::PB);
 #pragma unroll
                         for (int i = 0; i < C / 16; ++i) mma_ss(tmu + F::O2, vd + i * (2048 >> 4), pd + i * 2, id_o2, i > 0);
+#pragma unroll
+                        for (int i = 0; i < C / 16; ++i)
+                            mma_ss(tmu + F::O2, vd + i * (2048 >> 4), pd + (F::PB >> 4) + i * 2, id_o2, 1u);
                         mma_commit(&o_full);
                         mma_commit(&p_free[g & 1]);
                     }
@@ -508,14 +511,24 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 const int row = 32 * w + lane;
                 uint8_t* p0 = sm + F::P0 + row * 128;
                 if (w == 0)
-                    for (int b = 0; b < 2; ++b)
+                    for (int b = 0; b < 4; ++b)
                         for (int i = 4; i < 8; ++i)
                             *reinterpret_cast<uint4*>(p0 + b * F::PB + ((i ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                auto put = [&](uint8_t* p, int j0, const uint32_t (&u)[8]) {
+                // sixteen columns as two bf16 parts: x, and what its rounding left
+                auto put = [&](uint8_t* p, int j0, const float (&x)[16]) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        *reinterpret_cast<uint4*>(p + (((j0 / 8 + i) ^ (row & 7)) << 4)) =
-                            make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t u[4], r[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float x0 = x[8 * i + 2 * j], x1 = x[8 * i + 2 * j + 1];
+                            u[j] = pack_bf16x2(x0, x1);
+                            r[j] = pack_bf16x2(x0 - lo_f32(u[j]), x1 - hi_f32(u[j]));
+                        }
+                        uint8_t* at = p + (((j0 / 8 + i) ^ (row & 7)) << 4);
+                        *reinterpret_cast<uint4*>(at) = make_uint4(u[0], u[1], u[2], u[3]);
+                        *reinterpret_cast<uint4*>(at + F::PB) = make_uint4(r[0], r[1], r[2], r[3]);
+                    }
                 };
                 int s = 0, ph = 0, g = 0;
                 LinItem it;
@@ -530,40 +543,40 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     const float gr = d.g2[row];
                     const uint32_t at = tm + F::SP + (static_cast<uint32_t>(32 * w) << 16);
                     if (g >= 2 && !(ok = bar_wait(&p_free[g & 1], ((g >> 1) - 1) & 1))) break;
-                    uint8_t* p = p0 + (g & 1) * F::PB;
+                    uint8_t* p = p0 + (g & 1) * 2 * F::PB;
                     // sixteen columns a turn: left of the diagonal block (second warp) the factor is a product of
                     // two, each at most 1, about g_32
                     const float er = ex2_approx(gr - d.g2m);
 #pragma unroll 1
                     for (int j0 = 0; j0 < 32 * w; j0 += 16) {
                         float x[16];
-                        uint32_t u[8];
                         tmem_ld16(at + j0, x);
                         tmem_wait_ld_regs<16>(x);
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
                             const float4 m = *reinterpret_cast<const float4*>(&d.m[j0 + j]);
-                            u[j / 2] = pack_bf16x2(x[j] * (er * m.x), x[j + 1] * (er * m.y));
-                            u[j / 2 + 1] = pack_bf16x2(x[j + 2] * (er * m.z), x[j + 3] * (er * m.w));
+                            x[j] *= er * m.x;
+                            x[j + 1] *= er * m.y;
+                            x[j + 2] *= er * m.z;
+                            x[j + 3] *= er * m.w;
                         }
-                        put(p, j0, u);
+                        put(p, j0, x);
                     }
 #pragma unroll 1
                     for (int j0 = 32 * w; j0 < 32 * w + 32; j0 += 16) {
                         float x[16];
-                        uint32_t u[8];
                         tmem_ld16(at + j0, x);
                         tmem_wait_ld_regs<16>(x);
                         const int k = row - j0;   // the row's own column: what lies behind it is cut off
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
                             const float4 gj = *reinterpret_cast<const float4*>(&d.g2[j0 + j]);
-                            u[j / 2] = pack_bf16x2(j <= k ? x[j] * ex2_approx(gr - gj.x) : 0.f,
-                                                   j + 1 <= k ? x[j + 1] * ex2_approx(gr - gj.y) : 0.f);
-                            u[j / 2 + 1] = pack_bf16x2(j + 2 <= k ? x[j + 2] * ex2_approx(gr - gj.z) : 0.f,
-                                                       j + 3 <= k ? x[j + 3] * ex2_approx(gr - gj.w) : 0.f);
+                            x[j] = j <= k ? x[j] * ex2_approx(gr - gj.x) : 0.f;
+                            x[j + 1] = j + 1 <= k ? x[j + 1] * ex2_approx(gr - gj.y) : 0.f;
+                            x[j + 2] = j + 2 <= k ? x[j + 2] * ex2_approx(gr - gj.z) : 0.f;
+                            x[j + 3] = j + 3 <= k ? x[j + 3] * ex2_approx(gr - gj.w) : 0.f;
                         }
-                        put(p, j0, u);
+                        put(p, j0, x);
                     }
                     tc_fence_before();
                     warp_arrive(&sp_free);
