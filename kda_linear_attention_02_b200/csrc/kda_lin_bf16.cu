@@ -514,10 +514,10 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     for (int b = 0; b < 4; ++b)
                         for (int i = 4; i < 8; ++i)
                             *reinterpret_cast<uint4*>(p0 + b * F::PB + ((i ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                // sixteen columns as two bf16 parts: x, and what its rounding left
-                auto put = [&](uint8_t* p, int j0, const float (&x)[16]) {
+                // 32 columns from 8 b on, as two bf16 parts: x, and what its rounding left
+                auto put = [&](uint8_t* p, int b, const float (&x)[32]) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         uint32_t u[4], r[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -525,7 +525,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                             u[j] = pack_bf16x2(x0, x1);
                             r[j] = pack_bf16x2(x0 - lo_f32(u[j]), x1 - hi_f32(u[j]));
                         }
-                        uint8_t* at = p + (((j0 / 8 + i) ^ (row & 7)) << 4);
+                        uint8_t* at = p + (((b + i) ^ (row & 7)) << 4);
                         *reinterpret_cast<uint4*>(at) = make_uint4(u[0], u[1], u[2], u[3]);
                         *reinterpret_cast<uint4*>(at + F::PB) = make_uint4(r[0], r[1], r[2], r[3]);
                     }
@@ -539,47 +539,41 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 for (int c = (it.n + C - 1) / C; c > 0; --c, ++g) {
                     if (!(ok = bar_wait(&full[s], ph) && bar_wait(&sp_full, g & 1))) break;
                     tc_fence_after();
-                    const Decays& d = decays[g % F::ND];
-                    const float gr = d.g2[row];
+                    // the scores first, so that the next ones can be formed: the diagonal block's 32 columns, and those
+                    // left of it (second warp)
                     const uint32_t at = tm + F::SP + (static_cast<uint32_t>(32 * w) << 16);
-                    if (g >= 2 && !(ok = bar_wait(&p_free[g & 1], ((g >> 1) - 1) & 1))) break;
-                    uint8_t* p = p0 + (g & 1) * 2 * F::PB;
-                    // sixteen columns a turn: left of the diagonal block (second warp) the factor is a product of
-                    // two, each at most 1, about g_32
-                    const float er = ex2_approx(gr - d.g2m);
-#pragma unroll 1
-                    for (int j0 = 0; j0 < 32 * w; j0 += 16) {
-                        float x[16];
-                        tmem_ld16(at + j0, x);
-                        tmem_wait_ld_regs<16>(x);
-#pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 m = *reinterpret_cast<const float4*>(&d.m[j0 + j]);
-                            x[j] *= er * m.x;
-                            x[j + 1] *= er * m.y;
-                            x[j + 2] *= er * m.z;
-                            x[j + 3] *= er * m.w;
-                        }
-                        put(p, j0, x);
-                    }
-#pragma unroll 1
-                    for (int j0 = 32 * w; j0 < 32 * w + 32; j0 += 16) {
-                        float x[16];
-                        tmem_ld16(at + j0, x);
-                        tmem_wait_ld_regs<16>(x);
-                        const int k = row - j0;   // the row's own column: what lies behind it is cut off
-#pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 gj = *reinterpret_cast<const float4*>(&d.g2[j0 + j]);
-                            x[j] = j <= k ? x[j] * ex2_approx(gr - gj.x) : 0.f;
-                            x[j + 1] = j + 1 <= k ? x[j + 1] * ex2_approx(gr - gj.y) : 0.f;
-                            x[j + 2] = j + 2 <= k ? x[j + 2] * ex2_approx(gr - gj.z) : 0.f;
-                            x[j + 3] = j + 3 <= k ? x[j + 3] * ex2_approx(gr - gj.w) : 0.f;
-                        }
-                        put(p, j0, x);
-                    }
+                    float xd[32], xl[32];
+                    tmem_ld32(at + 32 * w, xd);
+                    if (w == 1) tmem_ld32(at, xl);
+                    tmem_wait_ld_regs<32>(xd);
+                    if (w == 1) tmem_wait_ld_regs<32>(xl);
                     tc_fence_before();
                     warp_arrive(&sp_free);
+                    const Decays& d = decays[g % F::ND];
+                    const float gr = d.g2[row];
+                    if (g >= 2 && !(ok = bar_wait(&p_free[g & 1], ((g >> 1) - 1) & 1))) break;
+                    uint8_t* p = p0 + (g & 1) * 2 * F::PB;
+                    if (w == 1) {   // a factor of two parts, each at most 1, about g_32
+                        const float er = ex2_approx(gr - d.g2m);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 m = *reinterpret_cast<const float4*>(&d.m[j]);
+                            xl[j] *= er * m.x;
+                            xl[j + 1] *= er * m.y;
+                            xl[j + 2] *= er * m.z;
+                            xl[j + 3] *= er * m.w;
+                        }
+                        put(p, 0, xl);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {   // what lies behind the row's own column is cut off
+                        const float4 gj = *reinterpret_cast<const float4*>(&d.g2[32 * w + j]);
+                        xd[j] = j <= lane ? xd[j] * ex2_approx(gr - gj.x) : 0.f;
+                        xd[j + 1] = j + 1 <= lane ? xd[j + 1] * ex2_approx(gr - gj.y) : 0.f;
+                        xd[j + 2] = j + 2 <= lane ? xd[j + 2] * ex2_approx(gr - gj.z) : 0.f;
+                        xd[j + 3] = j + 3 <= lane ? xd[j + 3] * ex2_approx(gr - gj.w) : 0.f;
+                    }
+                    put(p, 4 * w, xd);
                     fence_proxy_async_smem();
                     warp_arrive(&p_ready[g & 1]);
                     if (++s == NST) {
@@ -807,13 +801,15 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 ck_room = first >= 0 ? a.ckpt_cu[it.seq + 1] - first : 0;
                 ck = a.checkpoints + (static_cast<long long>(first) * a.H + h) * (DK * DV);
             }
-            int left = it.n;   // without tokens the state stays as it was
+            // A chunk's checkpoint and the segment's end are written once the next chunk's products have their copy of
+            // the state; without tokens the state stays as it was.
+            float *dst = nullptr, *last = it.n > 0 ? nullptr : end;
 #pragma unroll 1
-            do {
-                float* dst = nullptr;
+            for (int left = it.n;; left -= C) {
+                float eC = 0.f;
                 if (left > 0) {
                     if (!(ok = bar_wait(&full[s], ph))) break;   // before Sb lets the chunk's products go ahead (see `leave`)
-                    const float eC = decays[g % F::ND].eC;
+                    eC = decays[g % F::ND].eC;
                     if (BOUNDARY) {
                         warp_arrive(&empty[s]);
                     } else {
@@ -821,6 +817,18 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         tc_fence_after();
                         publish();
                     }
+                }
+                if (mine && (dst || last)) {
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {
+                        float* p = k == 0 ? dst : last;
+                        if (p)
+#pragma unroll
+                            for (int i = 0; i < DK; ++i) p[i * DV + ch] = S[i];
+                    }
+                }
+                if (left <= 0) break;
+                {
                     if (!(ok = bar_wait(&z_full[g & 1], (g >> 1) & 1))) break;
                     if (mine) {
                         tc_fence_after();
@@ -846,6 +854,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     }
                     ++g;
                     to_ck -= C;
+                    dst = nullptr;
                     if (!BOUNDARY && to_ck == 0 && left >= C) {
                         to_ck = a.ckpt_stride;
                         if (ck_room > 0) dst = ck;
@@ -854,19 +863,8 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         ck += static_cast<size_t>(a.H) * (DK * DV);
                     }
                 }
-                // a checkpoint, and the state at the segment's end
-                float* const last = left <= C ? end : nullptr;
-                if (mine && (dst || last)) {
-#pragma unroll 1
-                    for (int k = 0; k < 2; ++k) {
-                        float* p = k == 0 ? dst : last;
-                        if (p)
-#pragma unroll
-                            for (int i = 0; i < DK; ++i) p[i * DV + ch] = S[i];
-                    }
-                }
-                left -= C;
-            } while (left > 0);
+                last = left <= C ? end : nullptr;
+            }
         }
     }
     if (!ok && lane == 0) set_status(a.status, KDA_ERR_TIMEOUT);
