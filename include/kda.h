@@ -272,9 +272,10 @@ KDA_API kda_status_t kda_segment_compose(const float* transitions, const float* 
  *
  * kda_lin_chunk_fwd: the chunked form over a packed batch; cu_seqlens, initial_state, final_state,
  *   ckpt_stride, checkpoints and ckpt_cu as in kda_chunk_fwd.  Sequences of length 0 are allowed (the
- *   final state is the initial one).  initial_state and final_state must not overlap (KDA_ERR_ARG).  The states are accumulated in fp32 from exact products for both
- *   types; a bf16 call rounds the scores inside a chunk and the state that q is multiplied with once each to
- *   bf16 on the way to o.  q, k, v, o, states and checkpoints are 16-byte aligned, the workspace (at least
+ *   final state is the initial one).  initial_state and final_state must not overlap (KDA_ERR_ARG).  The
+ *   states are accumulated in fp32 from exact products for both types; a bf16 call rounds the state that q is
+ *   multiplied with once to bf16 on the way to o, and keeps the decayed scores inside a chunk to 16 bits (two
+ *   bf16 parts).  q, k, v, o, states and checkpoints are 16-byte aligned, the workspace (at least
  *   kda_lin_chunk_fwd_workspace_bytes, contents ignored) 256-byte aligned.  Results do not depend on what
  *   else is in the batch except through the split of long sequences into segments, which depends on
  *   (total_tokens, n_seqs, H) and changes the order of fp32 sums only.

@@ -4,19 +4,21 @@
 // tokens 1..t of the chunk, all products are written transposed, channels of v in the accumulator's lanes:
 //
 //     scores   s_tj = q_t . k_j                                   (SP, tokens t in lanes)
-//     P_tj     = e^{g_t - g_j} s_tj  (j <= t), rounded to bf16
+//     P_tj     = e^{g_t - g_j} s_tj  (j <= t), in two bf16 parts
 //     o_t      = e^{g_t} (S^T q_t)  +  sum_j P_tj v_j             (O1 = Sb Q^T, O2 = V^T P^T)
 //     S^T     <- e^{g_C} S^T + sum_j (e^{g_C - g_j} v_j) k_j^T    (Z = W K, W_j = e^{g_C - g_j} v_j)
 //
 // S^T stays in fp32 registers (thread = channel of v, register = channel of k); its bf16 copy Sb goes to
 // tensor memory as O1's A operand, in the lane layout the registers already have, and W is an A operand there
-// too.  What reaches o is rounded once in each path (P, and the copy of S).  What reaches the state is not: k
-// and v are bf16 already, and W goes in as four bf16 parts that add up to w v to 24 bits, so Z is an fp32 sum
+// too.  On the way to o the copy of S is rounded once, channel by channel, and such errors average out over the
+// sum.  P's would not: one P_tj weighs all of v_j, so with a single bf16 part an output that one token dominates
+// would be off by up to 2^-8 in every channel; a second part leaves 2^-16 and costs 2 % of the time.  What reaches
+// the state is not rounded: k and v are bf16 already, and W goes in as four bf16 parts that add up to w v to 24 bits, so Z is an fp32 sum
 // of exact products.  With w = w1 + w2 + w3 in bf16 parts, packed bf16 FMAs give them two tokens at a time,
 //     h = rn(w1 v),  -e = h - w1 v (exact: eight bits are left),  m = rn(w2 v),  -l = rn((m - w2 v) - w3 v),
-// five instructions a pair (splitting the fp32 products w v takes seventeen); the MMAs negate -e and -l.  Z starts from zero in every chunk and joins S by one rounded FMA: an
-// accumulator that lived on in tensor memory would collect the truncation of its additions over the length of
-// the sequence.
+// five instructions a pair (splitting the fp32 products w v takes seventeen); the MMAs negate -e and
+// -l.  Z starts from zero in every chunk and joins S by one rounded FMA: an accumulator that lived on in tensor
+// memory would collect the truncation of its additions over the length of the sequence.
 //
 // The grid has a CTA per SM; each takes (segment, head) pairs from a counter, longest first, until none is left,
 // and its copies run ahead into the next pair while the last chunks of one are worked on.

@@ -64,6 +64,29 @@ def test_chunk_shapes(dtype, dk, dv, lens):
     verify(x, call(x, outputs(x)))
 
 
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("decay", ["token", "fast"])
+def test_a_single_chunk_rounds_o_once(dk, dv, decay):
+    # From a zero state o is made of the scores alone, which keep 16 bits (two bf16 parts: half a step of the second
+    # is 2^-8 of what the first left, at most 2^-8).  The exponents are differences of sums of logarithms, each off by
+    # at most seven roundings (six additions of a scan and a product): 14 half steps of the largest sum.  What is left
+    # is o's own rounding, half a bf16 step.
+    lens = [1, 2, 3, 5, 64, 33, 1]
+    x = make(lens, 1, 2, dk, dv, BF, decay, init=False, seed=12)
+    y = call(x, outputs(x))
+    torch.cuda.synchronize()
+    o, b = ref.run(x["q"], x["k"], x["v"], x["la"], x["cu"], None)[:2]
+    g = max(float(s.sum(0).abs().max()) for s in x["la"].clamp_min(ref.LOG_MIN).split(lens))
+    tol = (2.0 ** -16 + ref.f32_factor(64, dk) + 14 * g * 2.0 ** -24) * b * (1 + 2.0 ** -8) + 2.0 ** -8 * o.abs() + 1e-30
+    ref.check("o", y["o"], o, tol)
+
+
+def test_stores_ahead_of_ragged_ends():
+    # pairs that end in a ragged chunk, which writes o without a tile store, several for each CTA
+    x = make([129, 191, 65, 130, 257, 70] * 8, 8, 8, 128, 128, BF, init=False, seed=13)
+    verify(x, call(x, outputs(x)))
+
+
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("Hqk,H", [(1, 1), (1, 6), (3, 6)])
 @pytest.mark.parametrize("decay", ["token", "fast", "head"])
