@@ -100,6 +100,21 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// Two products with the same A, one behind the other: the first leaves A in the collector buffer for the second.
+__device__ __forceinline__ void mma_ss_keep(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16.collector::a::fill [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ss_kept(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16.collector::a::lastuse [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+}
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -274,8 +289,8 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ Decays decays[F::ND];
     __shared__ __align__(8) float la_ring[4 * C];
-    __shared__ __align__(8) uint64_t full[NST], empty[NST], sp_full, sp_free, p_ready[2], p_free[2], w_go[2], w_free[2], z_free[2],
-        z_full[2], o_go, sb_free, o_full, done, job_full[2], job_free[2], w_sync, o_sync;
+    __shared__ __align__(8) uint64_t full[NST], empty[NST], sp_full, sp_free, w_go[2], w_free, z_free[2],
+        z_full[2], o_go[2], o_full[2], done, job_full[2], job_free[2], w_sync, o_sync;
     __shared__ Job jobs[2];
     __shared__ uint32_t tmem_slot;
     const int t = threadIdx.x, w = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
@@ -288,17 +303,17 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         }
         mbar_init(&sp_full, 1);
         mbar_init(&sp_free, kPWarps);
+        // The issuer's waits and commits are what a chunk's time is made of, so there are few.
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&p_ready[b], kPWarps);
-            mbar_init(&p_free[b], 1);
-            mbar_init(&w_go[b], kWWarps);
-            mbar_init(&w_free[b], 1);
-            mbar_init(&z_free[b], kSWarps);
-            mbar_init(&z_full[b], 1);
+            // the tokens' half of W is in place (b = 0 of the full pass: and Z of the chunk before has been read)
+            mbar_init(&w_go[b], kWWarps + (BOUNDARY || b ? 0 : kSWarps));
+            mbar_init(&z_free[b], kSWarps);   // boundary pass
+            mbar_init(&z_full[b], 1);         // Z is there, and W's second half free again
+            // Sb and P are in place, and O1, O2 of the chunk before have been read
+            mbar_init(&o_go[b], kOWarps + kSWarps + kPWarps);
+            mbar_init(&o_full[b], 1);         // O1 and O2 are there, and Sb and this P free again
         }
-        mbar_init(&o_go, kOWarps + kSWarps);   // Sb is in place, and O1, O2 of the chunk before have been read
-        mbar_init(&sb_free, 1);
-        mbar_init(&o_full, 1);
+        mbar_init(&w_free, 1);                // W's first half
         mbar_init(&done, 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&job_full[b], 1);
@@ -441,12 +456,12 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                             mma_ts(zcol, tmu + F::W + 32 * (i >> 1) + 8 * sl, kd + sl * (2048 >> 4), id_z | ((i & 2) ? neg_a : 0u),
                                    half + i > 0);
                         }
-                        mma_commit(&w_free[half]);
                     };
                     if (!(ok = bar_wait(&w_go[0], g & 1) &&
-                               (g < F::NZ || bar_wait(&z_free[g % F::NZ], (g / F::NZ - 1) & 1))))
+                               (!BOUNDARY || g < F::NZ || bar_wait(&z_free[g % F::NZ], (g / F::NZ - 1) & 1))))
                         break;
                     z_half(0);
+                    mma_commit(&w_free);
                     if (!BOUNDARY && c + 1 < nch) {
                         if (!(ok = bar_wait(&full[s1], ph1) && bar_wait(&sp_free, g & 1))) break;
                         tc_fence_after();
@@ -456,7 +471,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     z_half(1);
                     mma_commit(&z_full[g & 1]);
                     if (!BOUNDARY) {
-                        if (!(ok = bar_wait(&o_go, g & 1))) break;
+                        if (!(ok = bar_wait(&o_go[g & 1], (g >> 1) & 1))) break;
                         tc_fence_after();
                         const uint64_t qd = sdesc_k_sw128(q);
 #pragma unroll 1
@@ -464,17 +479,13 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
 #pragma unroll
                             for (uint32_t i = 0; i < 4; ++i)
                                 mma_ts(tmu + F::O1, tmu + F::SB + 32 * b + 8 * i, qd + b * (F::HALF >> 4) + 2 * i, id_o, b + i > 0);
-                        mma_commit(&sb_free);
-                        if (!(ok = bar_wait(&p_ready[g & 1], (g >> 1) & 1))) break;
-                        tc_fence_after();
                         const uint64_t vd = sdesc_mn_sw128(v, F::HALF), pd = sdesc_k_sw128(base + F::P0 + (g & 1) * 2 * F::PB);
 #pragma unroll
-                        for (int i = 0; i < C / 16; ++i) mma_ss(tmu + F::O2, vd + i * (2048 >> 4), pd + i * 2, id_o2, i > 0);
-#pragma unroll
-                        for (int i = 0; i < C / 16; ++i)
-                            mma_ss(tmu + F::O2, vd + i * (2048 >> 4), pd + (F::PB >> 4) + i * 2, id_o2, 1u);
-                        mma_commit(&o_full);
-                        mma_commit(&p_free[g & 1]);
+                        for (int i = 0; i < C / 16; ++i) {
+                            mma_ss_keep(tmu + F::O2, vd + i * (2048 >> 4), pd + i * 2, id_o2, i > 0);
+                            mma_ss_kept(tmu + F::O2, vd + i * (2048 >> 4), pd + (F::PB >> 4) + i * 2, id_o2, 1u);
+                        }
+                        mma_commit(&o_full[g & 1]);
                     }
                     mma_commit(&empty[s]);
                     s = s1;
@@ -553,7 +564,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     warp_arrive(&sp_free);
                     const Decays& d = decays[g % F::ND];
                     const float gr = d.g2[row];
-                    if (g >= 2 && !(ok = bar_wait(&p_free[g & 1], ((g >> 1) - 1) & 1))) break;
+                    if (g >= 2 && !(ok = bar_wait(&o_full[g & 1], ((g >> 1) - 1) & 1))) break;
                     uint8_t* p = p0 + (g & 1) * 2 * F::PB;
                     if (w == 1) {   // a factor of two parts, each at most 1, about g_32
                         const float er = ex2_approx(gr - d.g2m);
@@ -577,7 +588,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     }
                     put(p, 4 * w, xd);
                     fence_proxy_async_smem();
-                    warp_arrive(&p_ready[g & 1]);
+                    warp_arrive(&o_go[g & 1]);
                     if (++s == NST) {
                         s = 0;
                         ph ^= 1;
@@ -658,7 +669,10 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                             else if (half + 32 < to) load_v(row0, half + 32);
                         }
                     }
-                    if (g > 0) wait(&w_free[half >> 5], (g - 1) & 1);
+                    if (g > 0) {
+                        if (half == 0) wait(&w_free, (g - 1) & 1);
+                        else wait(&z_full[(g - 1) & 1], ((g - 1) >> 1) & 1);
+                    }
                     if (mine && ok) {
                         tc_fence_after();
 #pragma unroll
@@ -681,21 +695,21 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             // ---------------- o
             // Leave for o of chunk c is given with the chunk's decays in sight: a stage is filled anew as soon as its
             // products are done, so nobody may look for a filling after it has let those go ahead.
-            auto leave = [&]() {
+            auto leave = [&](int n) {
                 wait(&full[s], ph);
                 if (++s == NST) {
                     s = 0;
                     ph ^= 1;
                 }
-                warp_arrive(&o_go, ok);
+                warp_arrive(&o_go[n & 1], ok);
             };
 #pragma unroll 1
             for (int job = 0; ok && next_job(job, it, h); ++job) {
-            if (it.n > 0) leave();
+            if (it.n > 0) leave(g);
 #pragma unroll 1
             for (int left = it.n; left > 0 && ok; left -= C, ++g) {
                 const int tok = it.t0 + it.n - left;
-                wait(&o_full, g & 1);
+                wait(&o_full[g & 1], (g >> 1) & 1);
                 uint8_t* ob = sm + F::O0 + (g & 1) * F::VB;
                 // the store that read this buffer two chunks ago is done with it
                 if (tg == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
@@ -717,7 +731,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         tmem_wait_ld_regs<16>(y);
                         if (u4 == 3) {   // O1 and O2 have been read
                             tc_fence_before();
-                            if (left > C) leave();
+                            if (left > C) leave(g + 1);
                         }
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
@@ -732,7 +746,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         }
                     }
                 } else if (left > C) {
-                    leave();
+                    leave(g + 1);
                 }
                 fence_proxy_async_smem();
                 meet(&o_sync, met);
@@ -763,6 +777,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         const bool mine = ch < DV;
         const uint32_t lanes = static_cast<uint32_t>(32 * q4) << 16;
         float S[DK];
+        int s = 0, ph = 0, g = 0;
         auto publish = [&]() {   // the bf16 copy that O1 multiplies q with
             if (mine) {
 #pragma unroll
@@ -775,9 +790,9 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 tmem_wait_st();
                 tc_fence_before();
             }
-            warp_arrive(&o_go);
+            warp_arrive(&o_go[g & 1]);
         };
-        int s = 0, ph = 0, g = 0;
+        if (!BOUNDARY) warp_arrive(&w_go[0]);   // there is no Z yet
         LinItem it;
         int h;
 #pragma unroll 1
@@ -815,7 +830,8 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     if (BOUNDARY) {
                         warp_arrive(&empty[s]);
                     } else {
-                        if (g > 0 && !(ok = bar_wait(&sb_free, (g - 1) & 1))) break;   // the copy before has been read
+                        // the copy before has been read
+                        if (g > 0 && !(ok = bar_wait(&o_full[(g - 1) & 1], ((g - 1) >> 1) & 1))) break;
                         tc_fence_after();
                         publish();
                     }
@@ -849,7 +865,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                         }
                         tc_fence_before();
                     }
-                    warp_arrive(&z_free[g % F::NZ]);
+                    warp_arrive(BOUNDARY ? &z_free[g % F::NZ] : &w_go[0]);
                     if (++s == NST) {
                         s = 0;
                         ph ^= 1;
