@@ -278,7 +278,7 @@ kda_status_t kda_lin_recurrent_step(float* state, int64_t n_states, const int32_
     if (!aligned(state, 16) || !aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(o, es) ||
         !aligned(log_alpha, 4) || (slots && !aligned(slots, 4)))
         return KDA_ERR_ALIGN;
-    if (static_cast<long long>(n) * H * (dv / 32) > 0x7fffffffLL) return KDA_ERR_ARG;
+    if (static_cast<long long>(n) * H > 0x7fffffffLL) return KDA_ERR_ARG;
     int* st = status_ptr();
     if (!st) return KDA_ERR_CUDA;
     return launch_lin_step(state, n_states, slots, slot_stride, q, k, v, log_alpha, la_per_token, n, Hqk, H, dk, dv,

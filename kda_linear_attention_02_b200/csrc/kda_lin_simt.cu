@@ -13,6 +13,9 @@
 // dimension (8 16-byte reads for 64 FMAs; its rows are eight apart, so that neighbouring lanes read neighbouring
 // rows), and the quarters are joined in shared memory.  While a chunk is worked on, the next one's rows are
 // copied (cp.async) and a ninth warp forms the next one's decays.
+//
+// 3 sequences of up to 256 tokens x 2 heads of 64: 29 us for a call, 18 of them in the full pass: a chain of chunks on
+// 40 blocks.  4 x 4096 tokens x 8 heads of 128: 581 us, bound by the shared-memory reads (one output a thread: 1223).
 #include "kda_device.cuh"
 #include "kda_lin.h"
 
