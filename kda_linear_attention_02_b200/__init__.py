@@ -9,6 +9,7 @@ library has not been built the import of any entry point fails loudly.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -342,57 +343,58 @@ def kda_lin_chunk_fwd_workspace_bytes(total_tokens, n_seqs, H, dk, dv, dtype=KDA
                                                          int(dtype)))
 
 
-class _Launch:
-    """Where a call runs: the stream (the given one, else the current one of the tensors' device) as a raw pointer
-    in `.raw`, with that device current inside the with block.  The checks and the switch of device cost nothing
-    when the device is current already, which is what keeps the small calls short."""
-
-    __slots__ = ("raw", "stream", "dev", "back")
-
-    def __init__(self, t: torch.Tensor, name: str, stream):
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be on a CUDA device")
-        self.dev, self.stream, self.back = t.device, stream, None
-        if stream is None:
-            self.raw = torch._C._cuda_getCurrentRawStream(self.dev.index)
-        else:
-            if stream.device != self.dev:
-                raise ValueError(f"stream: expected device {self.dev}, got {stream.device}")
-            self.raw = stream.cuda_stream
-
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        if cur != self.dev.index:
-            self.back = cur
-            torch.cuda.set_device(self.dev.index)
-        return self
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
-
-    def empty(self, n, dtype=torch.uint8):
-        """A 1-D tensor that belongs to the call's stream: its memory is used again in that stream's order."""
-        if self.stream is None:
-            return torch.empty(n, dtype=dtype, device=self.dev)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(n, dtype=dtype, device=self.dev)
+# The calls below are a few microseconds on the device when the work is small, so their host side is kept short:
+# checks that cost little when they pass, device indices instead of device objects, sizes remembered by their numbers.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _same(t, name, shape, dtype, dev):
-    """_need for the hot calls: the checks first, the messages only when one fails."""
-    if t is None or t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
-        _need(t, name, shape, dtype, dev)
+def _enter(t: torch.Tensor, name: str, stream):
+    """Makes the tensor's device current; returns (the stream, or that device's current one, as a raw pointer, the
+    device to go back to or None)."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if stream is None:
+        raw = _raw_stream(dev)
+    else:
+        if stream.device != t.device:
+            raise ValueError(f"stream: expected device {t.device}, got {stream.device}")
+        raw = stream.cuda_stream
+    cur = _current_device()
+    if cur == dev:
+        return raw, None
+    torch.cuda.set_device(dev)
+    return raw, cur
+
+
+def _scratch(n, t, stream, dtype=torch.uint8):
+    """A 1-D tensor that belongs to the call's stream: its memory is used again in that stream's order."""
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=t.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=dtype, device=t.device)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace(query, *sizes):
+    return max(getattr(_load(), query)(*sizes), 256)
+
+
+def _same(t, name, shape, dtype, like):
+    """_need for the hot calls, on the device of `like`: the checks first, the messages only when one fails."""
+    if t is None or t.shape != shape or t.dtype is not dtype or t.get_device() != like.get_device() or not t.is_contiguous():
+        _need(t, name, shape, dtype, like.device)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _log_alpha(log_alpha, n, H, dev):
+def _log_alpha(log_alpha, n, H, like):
     """Checks log_alpha and tells whether it is per token ([n, H]) or a constant of each head ([H])."""
     per_token = log_alpha is None or log_alpha.dim() != 1
-    _same(log_alpha, "log_alpha", (n, H) if per_token else (H,), torch.float32, dev)
+    _same(log_alpha, "log_alpha", (n, H) if per_token else (H,), torch.float32, like)
     return int(per_token)
 
 
@@ -408,38 +410,42 @@ def kda_lin_chunk_fwd(q, k, v, log_alpha, initial_state, cu_seqlens, o, final_st
     _need(q, "q")
     if q.dim() != 3 or v is None or v.dim() != 3 or cu_seqlens is None:
         raise ValueError("q, v must be [T, heads, channels] and cu_seqlens [N + 1]")
-    dev, qt, f32 = q.device, q.dtype, torch.float32
+    qt, f32 = q.dtype, torch.float32
     T, Hqk, dk = q.shape
     _, H, dv = v.shape
     dt = _dtype_code(q)
     n = cu_seqlens.numel() - 1
-    _same(k, "k", (T, Hqk, dk), qt, dev)
-    _same(v, "v", (T, H, dv), qt, dev)
-    _same(o, "o", (T, H, dv), qt, dev)
-    per_token = _log_alpha(log_alpha, T, H, dev)
-    _same(cu_seqlens, "cu_seqlens", (n + 1,), torch.int32, dev)
+    _same(k, "k", (T, Hqk, dk), qt, q)
+    _same(v, "v", (T, H, dv), qt, q)
+    _same(o, "o", (T, H, dv), qt, q)
+    per_token = _log_alpha(log_alpha, T, H, q)
+    _same(cu_seqlens, "cu_seqlens", (n + 1,), torch.int32, q)
     if initial_state is not None:
-        _same(initial_state, "initial_state", (n, H, dk, dv), f32, dev)
+        _same(initial_state, "initial_state", (n, H, dk, dv), f32, q)
     if final_state is not None:
-        _same(final_state, "final_state", (n, H, dk, dv), f32, dev)
+        _same(final_state, "final_state", (n, H, dk, dv), f32, q)
     ck = cc = None
     if ckpt_stride:
-        _need(checkpoints, "checkpoints", None, f32, dev)
+        _need(checkpoints, "checkpoints", None, f32, q.device)
         if checkpoints.dim() != 4 or checkpoints.shape[1:] != (H, dk, dv):
             raise ValueError("checkpoints must be [n_ckpt, H, dk, dv]")
-        _same(ckpt_cu, "ckpt_cu", (n + 1,), torch.int32, dev)
+        _same(ckpt_cu, "ckpt_cu", (n + 1,), torch.int32, q)
         if checkpoints.numel():
             ck, cc = checkpoints.data_ptr(), ckpt_cu.data_ptr()
     L = _load()
-    with _Launch(q, "q", stream) as on:
+    raw, back = _enter(q, "q", stream)
+    try:
         if workspace is None:
-            workspace = on.empty(max(L.kda_lin_chunk_fwd_workspace_bytes(T, n, H, dk, dv, dt), 256))
+            workspace = _scratch(_workspace("kda_lin_chunk_fwd_workspace_bytes", T, n, H, dk, dv, dt), q, stream)
         else:
-            _need(workspace, "workspace", None, torch.uint8, dev)
+            _need(workspace, "workspace", None, torch.uint8, q.device)
         st = L.kda_lin_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), per_token,
                                  _ptr(initial_state), cu_seqlens.data_ptr(), n, T, Hqk, H, dk, dv, dt,
                                  int(ckpt_stride) if ck else 0, o.data_ptr(), _ptr(final_state), ck, cc,
-                                 workspace.data_ptr(), workspace.numel(), on.raw)
+                                 workspace.data_ptr(), workspace.numel(), raw)
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
     if st:
         _check(st, "kda_lin_chunk_fwd")
     return o
@@ -455,29 +461,33 @@ def kda_lin_recurrent_step(state, q, k, v, log_alpha, o, *, slots=None, stream=N
     _need(state, "state", None, torch.float32)
     if state.dim() != 4 or q is None or q.dim() != 3:
         raise ValueError("state must be [n_states, H, dk, dv] and q [n, Hqk, dk]")
-    dev, qt = state.device, q.dtype
+    qt = q.dtype
     n_states, H, dk, dv = state.shape
     n, Hqk, _ = q.shape
     dt = _dtype_code(q)
-    _same(q, "q", (n, Hqk, dk), qt, dev)
-    _same(k, "k", (n, Hqk, dk), qt, dev)
-    _same(v, "v", (n, H, dv), qt, dev)
-    _same(o, "o", (n, H, dv), qt, dev)
-    per_token = _log_alpha(log_alpha, n, H, dev)
+    _same(q, "q", (n, Hqk, dk), qt, state)
+    _same(k, "k", (n, Hqk, dk), qt, state)
+    _same(v, "v", (n, H, dv), qt, state)
+    _same(o, "o", (n, H, dv), qt, state)
+    per_token = _log_alpha(log_alpha, n, H, state)
     stride = 1
     if slots is not None:
-        if slots.shape != (n,) or slots.dtype != torch.int32 or slots.device != dev:
-            raise ValueError(f"slots must be int32 [{n}] on {dev}")
+        if slots.shape != (n,) or slots.dtype is not torch.int32 or slots.get_device() != state.get_device():
+            raise ValueError(f"slots must be int32 [{n}] on {state.device}")
         if n > 1:
             stride = slots.stride(0)
             if stride <= 0:
                 raise ValueError("slots: entries must not share memory")
     elif n > n_states:
         raise ValueError(f"{n} rows need as many states, got {n_states}")
-    with _Launch(state, "state", stream) as on:
+    raw, back = _enter(state, "state", stream)
+    try:
         st = _load().kda_lin_recurrent_step(state.data_ptr(), n_states, _ptr(slots), stride, q.data_ptr(), k.data_ptr(),
                                             v.data_ptr(), log_alpha.data_ptr(), per_token, n, Hqk, H, dk, dv, dt,
-                                            o.data_ptr(), on.raw)
+                                            o.data_ptr(), raw)
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
     if st:
         _check(st, "kda_lin_recurrent_step")
     return o
@@ -501,8 +511,7 @@ def kda_pages_copy(dst, src, dst_pages=None, src_pages=None, *, stream=None):
     that copy out, and one source may go to many destinations.
     """
     nb = _page_bytes(dst, "dst", 1)
-    dev = dst.device
-    _need(src, "src", None, dst.dtype, dev)
+    _need(src, "src", None, dst.dtype, dst.device)
     if src.shape[1:] != dst.shape[1:]:
         raise ValueError(f"src: expected pages of shape {tuple(dst.shape[1:])}, got {tuple(src.shape[1:])}")
     n = src.shape[0]
@@ -510,26 +519,30 @@ def kda_pages_copy(dst, src, dst_pages=None, src_pages=None, *, stream=None):
         if x is not None:
             n = x.numel()
     if dst_pages is not None:
-        _same(dst_pages, "dst_pages", (n,), torch.int32, dev)
+        _same(dst_pages, "dst_pages", (n,), torch.int32, dst)
     if src_pages is not None:
-        _same(src_pages, "src_pages", (n,), torch.int32, dev)
-    with _Launch(dst, "dst", stream) as on:
+        _same(src_pages, "src_pages", (n,), torch.int32, dst)
+    raw, back = _enter(dst, "dst", stream)
+    try:
         st = _load().kda_pages_copy(dst.data_ptr(), dst.shape[0], src.data_ptr(), src.shape[0], _ptr(dst_pages),
-                                    _ptr(src_pages), n, nb, on.raw)
+                                    _ptr(src_pages), n, nb, raw)
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
     if st:
         _check(st, "kda_pages_copy")
     return dst
 
 
-def _book(refs, table, counts, dev):
+def _book(refs, table, counts, like):
     """Checks the bookkeeping of a batch; returns (n_pages, n_rows, max_pages)."""
     if refs is None or table is None or refs.dim() != 1 or table.dim() != 2:
         raise ValueError("refs must be [n_pages] and table [n_rows, max_pages]")
     i32 = torch.int32
-    _same(refs, "refs", refs.shape, i32, dev)
-    _same(table, "table", table.shape, i32, dev)
+    _same(refs, "refs", refs.shape, i32, like)
+    _same(table, "table", table.shape, i32, like)
     rows, most = table.shape
-    _same(counts, "counts", (rows,), i32, dev)
+    _same(counts, "counts", (rows,), i32, like)
     return refs.shape[0], rows, most
 
 
@@ -544,41 +557,45 @@ def kda_pages_fork(pool, refs, table, counts, parents, children, n_shared=None, 
     row is extended.  A call that cannot be carried out changes nothing; kda_get_device_status tells why.
     """
     nb = _page_bytes(pool, "pool", 2)
-    dev, i32 = pool.device, torch.int32
-    n_pages, rows, most = _book(refs, table, counts, dev)
+    i32 = torch.int32
+    n_pages, rows, most = _book(refs, table, counts, pool)
     if n_pages != pool.shape[1]:
         raise ValueError(f"refs: expected {pool.shape[1]} pages, got {n_pages}")
-    _need(parents, "parents", None, i32, dev)
-    n = parents.numel()
-    _same(parents, "parents", (n,), i32, dev)
-    _same(children, "children", (n,), i32, dev)
+    n = 0 if parents is None else parents.numel()
+    _same(parents, "parents", (n,), i32, pool)
+    _same(children, "children", (n,), i32, pool)
     if n_shared is not None:
-        _same(n_shared, "n_shared", (n,), i32, dev)
+        _same(n_shared, "n_shared", (n,), i32, pool)
     if n_fresh is not None:
-        _same(n_fresh, "n_fresh", (n,), i32, dev)
+        _same(n_fresh, "n_fresh", (n,), i32, pool)
     L = _load()
-    with _Launch(pool, "pool", stream) as on:
+    raw, back = _enter(pool, "pool", stream)
+    try:
         if workspace is None:
-            workspace = on.empty(max(L.kda_pages_fork_workspace_bytes(n, most), 256))
+            workspace = _scratch(_workspace("kda_pages_fork_workspace_bytes", n, most), pool, stream)
         else:
-            _need(workspace, "workspace", None, torch.uint8, dev)
+            _need(workspace, "workspace", None, torch.uint8, pool.device)
         st = L.kda_pages_fork(pool.data_ptr(), pool.shape[0], n_pages, nb, refs.data_ptr(), table.data_ptr(),
                               counts.data_ptr(), rows, most, parents.data_ptr(), children.data_ptr(), _ptr(n_shared),
-                              _ptr(n_fresh), n, 1 if zero_fresh else 0, workspace.data_ptr(), workspace.numel(), on.raw)
+                              _ptr(n_fresh), n, 1 if zero_fresh else 0, workspace.data_ptr(), workspace.numel(), raw)
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
     if st:
         _check(st, "kda_pages_fork")
 
 
 def kda_pages_free(refs, table, counts, rows, *, stream=None):
     """Frees the rows: each of their pages loses a reference, their counts become 0 (C: kda_pages_free)."""
-    _need(refs, "refs")
-    dev = refs.device
-    n_pages, n_rows, most = _book(refs, table, counts, dev)
-    _need(rows, "rows", None, torch.int32, dev)
-    _same(rows, "rows", (rows.numel(),), torch.int32, dev)
-    with _Launch(refs, "refs", stream) as on:
+    n_pages, n_rows, most = _book(refs, table, counts, refs)
+    _same(rows, "rows", (0 if rows is None else rows.numel(),), torch.int32, refs)
+    raw, back = _enter(refs, "refs", stream)
+    try:
         st = _load().kda_pages_free(refs.data_ptr(), n_pages, table.data_ptr(), counts.data_ptr(), n_rows, most,
-                                    rows.data_ptr(), rows.shape[0], on.raw)
+                                    rows.data_ptr(), rows.shape[0], raw)
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
     if st:
         _check(st, "kda_pages_free")
 
@@ -590,25 +607,29 @@ def kda_pages_compact(pool, refs, table, counts, *, remap=None, n_live=None, wor
     here when None), n_live int32 [1] the number of pages in use.  Returns remap.
     """
     nb = _page_bytes(pool, "pool", 2)
-    dev, i32 = pool.device, torch.int32
-    n_pages, rows, most = _book(refs, table, counts, dev)
+    i32 = torch.int32
+    n_pages, rows, most = _book(refs, table, counts, pool)
     if n_pages != pool.shape[1]:
         raise ValueError(f"refs: expected {pool.shape[1]} pages, got {n_pages}")
     if n_live is not None:
-        _same(n_live, "n_live", (1,), i32, dev)
+        _same(n_live, "n_live", (1,), i32, pool)
     L = _load()
-    with _Launch(pool, "pool", stream) as on:
+    raw, back = _enter(pool, "pool", stream)
+    try:
         if remap is None:
-            remap = on.empty(n_pages, i32)
+            remap = _scratch(n_pages, pool, stream, i32)
         else:
-            _same(remap, "remap", (n_pages,), i32, dev)
+            _same(remap, "remap", (n_pages,), i32, pool)
         if workspace is None:
-            workspace = on.empty(max(L.kda_pages_compact_workspace_bytes(n_pages), 256))
+            workspace = _scratch(_workspace("kda_pages_compact_workspace_bytes", n_pages), pool, stream)
         else:
-            _need(workspace, "workspace", None, torch.uint8, dev)
+            _need(workspace, "workspace", None, torch.uint8, pool.device)
         st = L.kda_pages_compact(pool.data_ptr(), pool.shape[0], n_pages, nb, refs.data_ptr(), table.data_ptr(),
                                  counts.data_ptr(), rows, most, remap.data_ptr(), _ptr(n_live), workspace.data_ptr(),
-                                 workspace.numel(), on.raw)
+                                 workspace.numel(), raw)
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
     if st:
         _check(st, "kda_pages_compact")
     return remap
