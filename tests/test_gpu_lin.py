@@ -110,6 +110,32 @@ def test_chunk_long_sequences_run_in_segments(dtype, dk, dv, init):
     verify(x, call(x, outputs(x, 512), 512), 512)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_many_short_sequences_beside_a_long_one(dtype):
+    # more sequences than one block takes in a round, so that segments are not ordered by length
+    lens = [(7 * i) % 4 for i in range(2500)]
+    lens[1200] = 1300
+    x = make(lens, 1, 2, 64, 64, dtype, seed=14)
+    verify(x, call(x, outputs(x)))
+
+
+def test_calls_on_two_streams_at_once():
+    xs = [make([2100, 64, 1], 2, 4, 128, 128, BF, seed=20), make([900, 33] * 6, 4, 4, 64, 128, BF, "fast", seed=21),
+          make([1500, 7], 2, 2, 128, 64, F32, seed=22)]
+    want = [call(x, outputs(x)) for x in xs]
+    got = [[outputs(x) for x in xs] for _ in range(4)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for ys in got:
+        for x, y, s in zip(xs, ys, streams):
+            call(x, y, stream=s)
+    torch.cuda.synchronize()
+    assert kda.kda_get_device_status() == 0
+    for ys in got:
+        for y, w in zip(ys, want):
+            assert torch.equal(y["o"], w["o"]) and torch.equal(y["fs"], w["fs"])
+
+
 def test_resume_from_a_checkpoint():
     x = make([1000], 2, 4, 128, 128, BF, seed=4)
     full = call(x, outputs(x, 512), 512)
