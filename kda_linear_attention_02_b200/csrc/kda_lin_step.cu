@@ -2,7 +2,7 @@
 //
 // HBM-bound: a CTA streams one (row, head) state once in and once out, 16 bytes a load, all loads of a thread in
 // flight before the first use; the column sums of S^T q are joined over the row groups in shared memory.
-// 250 rows x 32 heads of 128 (1057 MB): 161 us = 6.56 TB/s, the rate of a plain copy.  One row: 9 us, the host's call.
+// 250 rows x 32 heads of 128 (1057 MB): 161 us = 6.56 TB/s, the rate of a plain copy.  One row: 8.4 us, the host's call.
 #include "kda_device.cuh"
 #include "kda_lin.h"
 
