@@ -432,6 +432,9 @@ def kda_lin_chunk_fwd(q, k, v, log_alpha, initial_state, cu_seqlens, o, final_st
         _same(ckpt_cu, "ckpt_cu", (n + 1,), torch.int32, q)
         if checkpoints.numel():
             ck, cc = checkpoints.data_ptr(), ckpt_cu.data_ptr()
+            for t, name in ((initial_state, "initial_state"), (final_state, "final_state")):
+                if t is not None and ck < t.data_ptr() + 4 * t.numel() and t.data_ptr() < ck + 4 * checkpoints.numel():
+                    raise ValueError(f"checkpoints and {name} must not overlap")
     L = _load()
     raw, back = _enter(q, "q", stream)
     try:

@@ -135,6 +135,16 @@ cudaError_t launch_chained(void (*kernel)(KArgs...), dim3 grid, dim3 block, cuda
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+// o is written while other heads, which may share q and k, are still read
+bool o_overlaps(const void* o, const void* q, const void* k, const void* v, int64_t tokens, int Hqk, int H, int dk, int dv,
+                bool bf16) {
+    const size_t row = static_cast<size_t>(tokens) * (bf16 ? 2 : 4), nq = row * Hqk * dk, nv = row * H * dv;
+    return overlap(o, nv, q, nq) || overlap(o, nv, k, nq) || overlap(o, nv, v, nv);
+}
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 bool dims_ok(int dk, int dv) { return (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }
@@ -223,12 +233,12 @@ kda_status_t kda_lin_chunk_fwd(const void* q, const void* k, const void* v, cons
         return KDA_ERR_ALIGN;
     if (!aligned(workspace, 256)) return KDA_ERR_ALIGN;
     // a later segment of a sequence may be done, and the final state written, before an earlier one starts
-    const uintptr_t st_bytes = static_cast<uintptr_t>(n_seqs) * H * dk * dv * sizeof(float);
-    const uintptr_t s0 = reinterpret_cast<uintptr_t>(initial_state), s1 = reinterpret_cast<uintptr_t>(final_state);
-    if (s0 && s1 && s0 < s1 + st_bytes && s1 < s0 + st_bytes) return KDA_ERR_ARG;
+    const size_t st_bytes = static_cast<size_t>(n_seqs) * H * dk * dv * sizeof(float);
+    if (overlap(initial_state, st_bytes, final_state, st_bytes)) return KDA_ERR_ARG;
     const bool bf16 = dtype == KDA_BF16;
     const LinLayout l = layout(total_tokens, n_seqs, H, dk, dv, bf16);
     if (ws_bytes < l.total) return KDA_ERR_WORKSPACE;
+    if (o_overlaps(o, q, k, v, total_tokens, Hqk, H, dk, dv, bf16)) return KDA_ERR_ARG;
     if (static_cast<long long>(l.max_items) * H > 0x7fffffffLL) return KDA_ERR_ARG;
 
     char* ws = static_cast<char*>(workspace);
@@ -279,6 +289,7 @@ kda_status_t kda_lin_recurrent_step(float* state, int64_t n_states, const int32_
         !aligned(log_alpha, 4) || (slots && !aligned(slots, 4)))
         return KDA_ERR_ALIGN;
     if (static_cast<long long>(n) * H > 0x7fffffffLL) return KDA_ERR_ARG;
+    if (o_overlaps(o, q, k, v, n, Hqk, H, dk, dv, dtype == KDA_BF16)) return KDA_ERR_ARG;
     int* st = status_ptr();
     if (!st) return KDA_ERR_CUDA;
     return launch_lin_step(state, n_states, slots, slot_stride, q, k, v, log_alpha, la_per_token, n, Hqk, H, dk, dv,

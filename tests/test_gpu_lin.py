@@ -208,6 +208,17 @@ def test_bad_sequence_tables_write_nothing(cu):
     assert y["o"].isnan().all() and y["fs"].isnan().all()
 
 
+def test_checkpoints_over_the_states_are_refused():
+    x = make([200, 200], 1, 1, 64, 64, BF)
+    pool = torch.zeros(8, 1, 64, 64, device=DEV)
+    y = outputs(x, 64)
+    y["ck"] = pool[:6]
+    for name, a, b in (("initial_state", pool[5:7], y["fs"]), ("final_state", x["init"], pool[5:7])):
+        x["init"], y["fs"] = a, b
+        with pytest.raises(ValueError, match=name):
+            call(x, y, 64)
+
+
 def test_bad_checkpoint_table_is_reported():
     x = make([200, 200], 1, 1, 64, 64, BF)
     y = outputs(x, 64)

@@ -39,6 +39,17 @@ def test_chunk_refusals(lib, over, want):
     assert chunk(lib, **over) == want
 
 
+@pytest.mark.parametrize("dt", [0, 1])
+@pytest.mark.parametrize("name,size", [("q", 100 * 2 * 128), ("k", 100 * 2 * 128), ("v", 100 * 4 * 128)])
+def test_outputs_over_inputs_are_refused(lib, dt, name, size):
+    # o [100, 4, 128] begins at the input, or 16 bytes ahead of the input's end, or ends 16 bytes behind its start
+    es, at = (2, 4)[dt], 1 << 30
+    apart = dict(q=1 << 32, k=2 << 32, v=3 << 32, dt=dt)
+    for o in (at, at + size * es - 16, at - 100 * 4 * 128 * es + 16):
+        assert chunk(lib, **{**apart, name: at, "o": o}) == ARG
+        assert step(lib, **{**apart, name: at, "o": o, "n": 100, "ns": 100}) == ARG
+
+
 def test_chunk_of_nothing_is_fine(lib):
     assert chunk(lib, n=0, T=0) == 0
 
