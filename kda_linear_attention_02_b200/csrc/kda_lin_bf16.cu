@@ -69,7 +69,6 @@ struct Cfg {
     static constexpr uint32_t SP = 0, O1 = 64, O2 = 128, SB = 320, W = 384, COLS = 512;
     static constexpr int NZ = BOUNDARY ? 2 : 1;
     static constexpr uint32_t Z = BOUNDARY ? 0 : 192;
-    static_assert(BYTES + 1024 + 4096 <= 227 * 1024, "shared memory");
 };
 constexpr int kThreads = 512;
 constexpr int kPWarps = 2, kWWarps = 4, kOWarps = 4, kSWarps = 4;
@@ -84,13 +83,14 @@ struct __align__(16) Job {   // a segment of one (sequence, head)
 };
 
 struct Decays {            // of one chunk
-    float g2[kChunk];      // g_t log2(e)
+    float g2[kChunk];      // g_t log2(e), as two numbers (see Log2)
+    float g2l[kChunk];
     float eg[kChunk];      // e^{g_t}
     uint4 w[kChunk / 2];   // of tokens 2 i, 2 i + 1: the bf16 parts w1, w2, -w3 of e^{g_C - g_t}, packed pairs
     float m[kChunk / 2];   // e^{g_32 - g_t} of the chunk's first half
-    float g2m;             // g_32 log2(e)
+    float g2m, g2ml;       // g_32 log2(e), likewise
     float eC;              // e^{g_C}
-    float pad[2];
+    float pad;
 };
 
 // fp32 pair -> packed bf16 pair, and back
@@ -205,22 +205,37 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, bool v
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
 }
 
-// e^x for x <= 0 to about one unit in the last place: 2^(x log2 e) with the rounding of the product put back.
-__device__ __forceinline__ float exp_fast(float x) {
+// A logarithm to base 2 as h + l, h a multiple of 2^-10, |l| about 2^-11 at most for one token.  What counts are
+// differences of a chunk's sums, and a token that forgets everything moves all later sums by 173: as plain fp32
+// numbers, forty of them would leave the differences behind them 10 bits.  The sums of h (below 2^14) are exact in
+// fp32, in any order, and those of l, below 2^-4, off by less than 2^-26, so that a difference is rounded once.
+struct Log2 {
+    float h, l;
+};
+__device__ __forceinline__ Log2 operator+(Log2 a, Log2 b) { return {a.h + b.h, a.l + b.l}; }
+__device__ __forceinline__ Log2 operator-(Log2 a, Log2 b) { return {a.h - b.h, a.l - b.l}; }
+__device__ __forceinline__ Log2 log2_of(float x) {   // of e^x
     const float y = x * kLog2e, r = fmaf(x, kLog2e, -y) + x * 1.9259629e-8f;   // log2(e) - kLog2e
-    const float e = ex2_approx(y);
+    const float h = __fadd_rn(__fadd_rn(y, 12288.f), -12288.f);                // ulp(12288 - 174) = 2^-10
+    return {h, (y - h) + r};
+}
+// 2^(h + l) to about one unit in the last place: the rounding of the sum is put back.
+__device__ __forceinline__ float exp2_of(Log2 x) {
+    const float y = x.h + x.l, r = (x.h - y) + x.l, e = ex2_approx(y);
     return fmaf(e, r * 0.69314718f, e);
 }
 
 // One warp's walk over the log_alpha of a segment: the decays of its chunks, in order.  Lane i has tokens 2 i and
 // 2 i + 1 of a chunk, and fetches theirs three chunks ahead (a load takes longer than a chunk), to shared memory,
 // since moving a value on in registers would wait for its load.
+// FULL: and what o needs of them.
+template <bool FULL>
 struct DecayWalk {
     const float* la;
     const float* any;      // a valid address for copies that read nothing
     int la_t, n, left, lane;
     float* ring;           // this lane's pair in the first of four slots of kChunk
-    float total;           // sum over the chunks so far
+    Log2 total;            // sum over the chunks so far
 
     __device__ __forceinline__ void fetch(int c) {
         const uint32_t at = smem_u32(ring + (c & 3) * kChunk);
@@ -239,7 +254,7 @@ struct DecayWalk {
         n = it.n;
         left = n - 2 * lane;
         ring = slots + 2 * lane;
-        total = 0.f;
+        total = {0.f, 0.f};
         if (n > 0)
 #pragma unroll 1
             for (int c = 0; c < 3; ++c) fetch(c);
@@ -249,23 +264,31 @@ struct DecayWalk {
         asm volatile("cp.async.wait_group 3;" ::: "memory");
         const float2 x = *reinterpret_cast<const float2*>(ring + (c & 3) * kChunk);
         const bool in0 = c * kChunk + 2 * lane < n, in1 = c * kChunk + 2 * lane + 1 < n;
-        const float x0 = in0 ? fmaxf(x.x, kLinLogMin) : 0.f, x1 = in1 ? fmaxf(x.y, kLinLogMin) : 0.f;
-        // inclusive sums of the lanes' pairs, from the chunk's start and from its end
-        float f = x0 + x1, r = f;
+        const Log2 x0 = log2_of(in0 ? fmaxf(x.x, kLinLogMin) : 0.f), x1 = log2_of(in1 ? fmaxf(x.y, kLinLogMin) : 0.f);
+        Log2 f = x0 + x1;   // inclusive sums of the lanes' pairs
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const float u = __shfl_up_sync(0xffffffffu, f, off), v = __shfl_down_sync(0xffffffffu, r, off);
-            if (lane >= off) f += u;
-            if (lane + off < 32) r += v;
+            const Log2 u = {__shfl_up_sync(0xffffffffu, f.h, off), __shfl_up_sync(0xffffffffu, f.l, off)};
+            if (lane >= off) f = f + u;
         }
-        float before = __shfl_up_sync(0xffffffffu, f, 1), after = __shfl_down_sync(0xffffffffu, r, 1);
-        if (lane == 0) before = 0.f;
-        if (lane == 31) after = 0.f;
-        const float sum = __shfl_sync(0xffffffffu, f, 31), gm = __shfl_sync(0xffffffffu, f, 15);
-        const float2 gt = make_float2(before + x0, f);
-        *reinterpret_cast<float2*>(&d.g2[2 * lane]) = make_float2(gt.x * kLog2e, gt.y * kLog2e);
-        *reinterpret_cast<float2*>(&d.eg[2 * lane]) = make_float2(exp_fast(gt.x), exp_fast(gt.y));
-        float w0 = exp_fast(after + x1), w1 = exp_fast(after);
+        auto of_lane = [&](int i) { return Log2{__shfl_sync(0xffffffffu, f.h, i), __shfl_sync(0xffffffffu, f.l, i)}; };
+        const Log2 sum = of_lane(31), g0 = f - x1;
+        float w0 = exp2_of(sum - g0), w1 = exp2_of(sum - f);
+        if (FULL) {
+            const Log2 gm = of_lane(15);
+            *reinterpret_cast<float2*>(&d.g2[2 * lane]) = make_float2(g0.h, f.h);
+            *reinterpret_cast<float2*>(&d.g2l[2 * lane]) = make_float2(g0.l, f.l);
+            *reinterpret_cast<float2*>(&d.eg[2 * lane]) = make_float2(exp2_of(g0), exp2_of(f));
+            if (lane < 16) {
+                const Log2 m0 = gm - g0, m1 = gm - f;
+                *reinterpret_cast<float2*>(&d.m[2 * lane]) = make_float2(ex2_approx(m0.h + m0.l), ex2_approx(m1.h + m1.l));
+            }
+            if (lane == 0) {
+                d.g2m = gm.h;
+                d.g2ml = gm.l;
+            }
+        }
+        if (lane == 0) d.eC = exp2_of(sum);
         uint32_t part[3];
 #pragma unroll
         for (int p = 0; p < 3; ++p) {
@@ -274,14 +297,7 @@ struct DecayWalk {
             w1 -= hi_f32(part[p]);
         }
         d.w[lane] = make_uint4(part[0], part[1], part[2] ^ 0x80008000u, 0u);
-        if (lane < 16)
-            *reinterpret_cast<float2*>(&d.m[2 * lane]) =
-                make_float2(ex2_approx((gm - gt.x) * kLog2e), ex2_approx((gm - gt.y) * kLog2e));
-        if (lane == 0) {
-            d.g2m = gm * kLog2e;
-            d.eC = exp_fast(sum);
-        }
-        total += sum;
+        total = total + sum;
     }
 };
 
@@ -291,6 +307,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
     using F = Cfg<DK, DV, BOUNDARY>;
     constexpr int NST = F::NST, C = F::C;
+    static_assert(F::BYTES + 1024 + F::ND * sizeof(Decays) + 2048 <= 227 * 1024, "shared memory, with 2 KB for barriers, pairs and the ring");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ Decays decays[F::ND];
@@ -376,7 +393,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     return;
                 }
             };
-            DecayWalk walk;
+            DecayWalk<true> walk;
             Job next;
             if (lane == 0) claim(true, next);
             int s = 0, ph = 1, g = 0;   // stage and its parity, chunks so far
@@ -503,7 +520,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
         } else if (BOUNDARY) {
             // ---------------- decays, where a chunk takes less time than forming them and issuing its copies
             if (w == 1) {
-                DecayWalk walk;
+                DecayWalk<false> walk;
                 LinItem it;
                 int h, s = 0, ph = 1, g = 0;
 #pragma unroll 1
@@ -520,7 +537,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                             ph ^= 1;
                         }
                     }
-                    if (lane == 0) a.zdecay[static_cast<size_t>(it.z0 + it.seg) * a.H + h] = exp_fast(walk.total);
+                    if (lane == 0) a.zdecay[static_cast<size_t>(it.z0 + it.seg) * a.H + h] = exp2_of(walk.total);
                 }
                 cp_async_wait_all();
             }
@@ -569,11 +586,11 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
                     tc_fence_before();
                     warp_arrive(&sp_free);
                     const Decays& d = decays[g % F::ND];
-                    const float gr = d.g2[row];
+                    const float gr = d.g2[row], gl = d.g2l[row];
                     if (g >= 2 && !(ok = bar_wait(&o_full[g & 1], ((g >> 1) - 1) & 1))) break;
                     uint8_t* p = p0 + (g & 1) * 2 * F::PB;
                     if (w == 1) {   // a factor of two parts, each at most 1, about g_32
-                        const float er = ex2_approx(gr - d.g2m);
+                        const float er = ex2_approx((gr - d.g2m) + (gl - d.g2ml));
 #pragma unroll
                         for (int j = 0; j < 32; j += 4) {
                             const float4 m = *reinterpret_cast<const float4*>(&d.m[j]);
@@ -587,10 +604,16 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {   // what lies behind the row's own column is cut off
                         const float4 gj = *reinterpret_cast<const float4*>(&d.g2[32 * w + j]);
-                        xd[j] = j <= lane ? xd[j] * ex2_approx(gr - gj.x) : 0.f;
-                        xd[j + 1] = j + 1 <= lane ? xd[j + 1] * ex2_approx(gr - gj.y) : 0.f;
-                        xd[j + 2] = j + 2 <= lane ? xd[j + 2] * ex2_approx(gr - gj.z) : 0.f;
-                        xd[j + 3] = j + 3 <= lane ? xd[j + 3] * ex2_approx(gr - gj.w) : 0.f;
+                        const float4 lj = *reinterpret_cast<const float4*>(&d.g2l[32 * w + j]);
+                        const float2 m1 = make_float2(-1.f, -1.f), gr2 = make_float2(gr, gr), gl2 = make_float2(gl, gl);
+                        auto diff = [&](float h0, float h1, float l0, float l1) {
+                            return __fadd2_rn(__ffma2_rn(m1, make_float2(h0, h1), gr2), __ffma2_rn(m1, make_float2(l0, l1), gl2));
+                        };
+                        const float2 e0 = diff(gj.x, gj.y, lj.x, lj.y), e1 = diff(gj.z, gj.w, lj.z, lj.w);
+                        xd[j] = j <= lane ? xd[j] * ex2_approx(e0.x) : 0.f;
+                        xd[j + 1] = j + 1 <= lane ? xd[j + 1] * ex2_approx(e0.y) : 0.f;
+                        xd[j + 2] = j + 2 <= lane ? xd[j + 2] * ex2_approx(e1.x) : 0.f;
+                        xd[j + 3] = j + 3 <= lane ? xd[j + 3] * ex2_approx(e1.y) : 0.f;
                     }
                     put(p, 4 * w, xd);
                     fence_proxy_async_smem();

@@ -1,0 +1,56 @@
+"""How many bits the bf16 chunks of the decayed linear attention keep, against the recurrence in 64 bits."""
+import pytest
+import torch
+
+import kda_linear_attention_02_b200 as kda
+import lin_reference as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def chunk(q, k, v, la, cu, init=None, stride=0):
+    """(o, final states, checkpoints) of a call that has to end well."""
+    T, H, dv = v.shape
+    n, dk = cu.numel() - 1, q.shape[2]
+    ckcu = kda.kda_ckpt_offsets(cu.cpu(), stride).to(DEV) if stride else None
+    o = torch.full((T, H, dv), float("nan"), dtype=v.dtype, device=DEV)
+    fs = torch.full((n, H, dk, dv), float("nan"), device=DEV)
+    ck = torch.full((int(ckcu[-1]), H, dk, dv), float("nan"), device=DEV) if stride else None
+    kda.kda_lin_chunk_fwd(q, k, v, la, init, cu, o, fs, ckpt_stride=stride, checkpoints=ck, ckpt_cu=ckcu)
+    torch.cuda.synchronize()
+    assert kda.kda_get_device_status() == 0
+    return o, fs, ck
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("resets", [0, 1, 8, 24, 31, 40, 56])
+@pytest.mark.parametrize("reset", [-100.0, float("-inf")])
+def test_scores_behind_forgotten_tokens_keep_their_bits(dk, dv, resets, reset):
+    # Some tokens at a chunk's start forget everything, the rest forget little.  q and k are unit vectors of one
+    # channel, so that every score is exactly 1 and a weight is the decay alone; two tokens behind the resets have
+    # values of opposite sign, so that o is the small difference of two weights and its own rounding hides nothing.
+    # A weight e^x, x >= -120, comes from an exponent that two roundings put off by at most 2 x 120 x 2^-24 < 2^-16,
+    # and is kept in two bf16 parts, 2^-8 of 2^-8; the rest is a few half steps of fp32 (the exponential two, the
+    # sums of two products one each).
+    H, n = 8, 64
+    g = torch.Generator(DEV)
+    g.manual_seed(resets)
+    la = -torch.exp(1.5 * torch.randn(2 * n, H, generator=g, device=DEV) - 6.0)
+    la[:resets], la[n:n + resets] = reset, reset
+    q = torch.zeros(2 * n, 1, dk, dtype=BF, device=DEV)
+    q[..., 3] = 1.0
+    v = torch.zeros(2 * n, H, dv, dtype=BF, device=DEV)
+    u = (1.0 + torch.rand(dv, generator=g, device=DEV)).to(BF)
+    for h in range(H):      # another pair for each head, in both sequences
+        i, j = resets + h * (n - 3 - resets) // H, resets + 1 + h * (n - 3 - resets) // H + h % 2
+        v[i, h], v[j, h], v[n + i, h], v[n + j, h] = u, -u, -u, u
+    cu = ints([0, n, 2 * n])
+    o, fs, _ = chunk(q, q, v, la, cu)
+    want, b, ws, aws, _, _ = ref.run(q, q, v, la, cu, None)
+    ref.check("o", o, want, (2.0 ** -16 + 2.0 ** -16 + 2.0 ** -20) * b + 2.0 ** -8 * want.abs() + 1e-30)
