@@ -286,6 +286,7 @@ KDA_API kda_status_t kda_segment_compose(const float* transitions, const float* 
  *   column of a page table can be passed.  A row with a negative slot is idle: nothing of it is read, its
  *   rows of o stay as they were.  A slot outside n_states, or one that two rows name, is an error: those
  *   rows are left out (state and o as they were) and the status word becomes KDA_ERR_DEVICE_INPUT.
+ *   n is at most 2^30, n H at most 2^31 - 1.
  *   state is 16-byte aligned; the per-token inputs need element alignment only.  o overlapping q, k or v is
  *   KDA_ERR_ARG.
  */
@@ -342,6 +343,7 @@ KDA_API kda_status_t kda_lin_recurrent_step(float* state, int64_t n_states, cons
  *   follow; remap [n_pages] receives each page's new number (-1 for free pages) and n_live (device, one
  *   int32, or NULL) the count.  A table entry out of range, or naming a free page, stays as it was and the
  *   status word becomes KDA_ERR_DEVICE_INPUT.
+ * n_pages and n are at most 2^30, n_rows of kda_pages_fork at most 2^20, n max_pages of it at most 2^30 (KDA_ERR_ARG).
  * The workspaces are 256-byte aligned device scratch of at least the bytes the queries give.
  */
 KDA_API kda_status_t kda_pages_copy(void* dst, int64_t n_dst, const void* src, int64_t n_src,

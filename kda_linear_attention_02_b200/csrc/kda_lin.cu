@@ -277,7 +277,7 @@ kda_status_t kda_lin_recurrent_step(float* state, int64_t n_states, const int32_
                                     const void* q, const void* k, const void* v, const float* log_alpha,
                                     int la_per_token, int n, int Hqk, int H, int dk, int dv, kda_dtype_t dtype,
                                     void* o, kda_stream_t stream) {
-    if (n < 0 || H <= 0 || Hqk <= 0 || H % Hqk != 0 || n_states < 0 || (la_per_token != 0 && la_per_token != 1))
+    if (n < 0 || n > 0x40000000 || H <= 0 || Hqk <= 0 || H % Hqk != 0 || n_states < 0 || (la_per_token != 0 && la_per_token != 1))
         return KDA_ERR_ARG;
     if (slots ? slot_stride <= 0 : n > n_states) return KDA_ERR_ARG;
     if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_ARG;

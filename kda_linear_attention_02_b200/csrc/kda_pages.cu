@@ -450,6 +450,7 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 constexpr size_t kHeadBytes = 256;
 constexpr int kMaxRows = 1 << 20;   // a bit for each row in one block's shared memory (128 KB)
 constexpr long long kMaxMoves = 1ll << 30;
+constexpr int kMaxList = 1 << 30;   // pages of a pool, entries of a list: what the kernels' 32-bit loops can step over
 
 size_t fork_bytes(int n, int max_pages) {
     return kHeadBytes + round256(sizeof(ForkEntry) * static_cast<size_t>(n)) +
@@ -466,7 +467,7 @@ unsigned move_blocks(size_t page_bytes, int n_planes, long long moves) {
 
 bool pool_ok(int n_planes, int n_pages, size_t page_bytes) {
     // every byte offset fits 63 bits
-    return n_planes > 0 && n_pages >= 0 && page_bytes > 0 && page_bytes % 16 == 0 && page_bytes <= (size_t{1} << 30) &&
+    return n_planes > 0 && n_pages >= 0 && n_pages <= kMaxList && page_bytes > 0 && page_bytes % 16 == 0 && page_bytes <= (size_t{1} << 30) &&
            static_cast<double>(page_bytes) * n_pages * n_planes < 9e18;
 }
 
@@ -480,7 +481,7 @@ extern "C" {
 
 kda_status_t kda_pages_copy(void* dst, int64_t n_dst, const void* src, int64_t n_src, const int32_t* dst_pages,
                             const int32_t* src_pages, int n, size_t page_bytes, kda_stream_t stream) {
-    if (n < 0 || n_dst < 0 || n_src < 0 || n_dst > 0x7fffffffLL || n_src > 0x7fffffffLL) return KDA_ERR_ARG;
+    if (n < 0 || n > kMaxList || n_dst < 0 || n_src < 0 || n_dst > 0x7fffffffLL || n_src > 0x7fffffffLL) return KDA_ERR_ARG;
     if (page_bytes == 0 || page_bytes % 16 != 0 || page_bytes > (size_t{1} << 30)) return KDA_ERR_ARG;
     if ((!dst_pages && n > n_dst) || (!src_pages && n > n_src)) return KDA_ERR_ARG;
     if (n == 0) return KDA_OK;
@@ -550,7 +551,7 @@ kda_status_t kda_pages_fork(void* pool, int n_planes, int n_pages, size_t page_b
 
 kda_status_t kda_pages_free(int32_t* refs, int n_pages, const int32_t* table, int32_t* counts, int n_rows, int max_pages,
                             const int32_t* rows, int n, kda_stream_t stream) {
-    if (n < 0 || n_pages < 0 || n_rows < 0 || max_pages <= 0) return KDA_ERR_ARG;
+    if (n < 0 || n > kMaxList || n_pages < 0 || n_pages > kMaxList || n_rows < 0 || max_pages <= 0) return KDA_ERR_ARG;
     if (n == 0) return KDA_OK;
     if ((!refs && n_pages > 0) || !rows || (n_rows > 0 && (!table || !counts))) return KDA_ERR_ARG;
     if (!aligned(refs, 4) || !aligned(table, 4) || !aligned(counts, 4) || !aligned(rows, 4)) return KDA_ERR_ALIGN;
@@ -561,7 +562,9 @@ kda_status_t kda_pages_free(int32_t* refs, int n_pages, const int32_t* table, in
                           counts, n_rows, max_pages, rows, n, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
-size_t kda_pages_compact_workspace_bytes(int n_pages) { return n_pages < 0 ? 0 : compact_bytes(n_pages); }
+size_t kda_pages_compact_workspace_bytes(int n_pages) {
+    return n_pages < 0 || n_pages > kMaxList ? 0 : compact_bytes(n_pages);
+}
 
 kda_status_t kda_pages_compact(void* pool, int n_planes, int n_pages, size_t page_bytes, int32_t* refs, int32_t* table,
                                const int32_t* counts, int n_rows, int max_pages, int32_t* remap, int32_t* n_live,
