@@ -246,10 +246,9 @@ __device__ __forceinline__ void draft_step(float4 (&s)[DecodeTiling<DK, DV, NT>:
 // [n, H, dv / 32]) and T is the type of o (bf16).
 template <typename T, int DK, int DV, bool MX>
 __global__ void __launch_bounds__(256, 2)
-decode_step_kernel(float* __restrict__ state, const void* __restrict__ q, const void* __restrict__ k,
-                   const void* __restrict__ v, const uint8_t* __restrict__ q_scale,
-                   const uint8_t* __restrict__ k_scale, const uint8_t* __restrict__ v_scale,
-                   const float* __restrict__ log_alpha, const float* __restrict__ beta, T* __restrict__ o) {
+decode_step_kernel(float* __restrict__ state, const void* q, const void* k, const void* v, const uint8_t* q_scale,
+                   const uint8_t* k_scale, const uint8_t* v_scale, const float* log_alpha, const float* beta,
+                   T* __restrict__ o) {
     using DT = DecodeTiling<DK, DV, 256>;
     __shared__ DecodeSmem<DK, DV, 256> sh;
     grid_dependency_wait();   // the state (and inputs) come from earlier launches
@@ -312,9 +311,8 @@ template <int DV>
 __host__ __device__ constexpr int spec_threads() { return 256 * kSpecSlice / DV; }
 template <typename T, int DK, int DV, bool VERIFY>
 __global__ void __launch_bounds__(spec_threads<DV>(), 1024 / spec_threads<DV>() / 2)
-decode_multi_kernel(float* __restrict__ state, const T* __restrict__ q, const T* __restrict__ k,
-                    const T* __restrict__ v, const float* __restrict__ log_alpha, const float* __restrict__ beta,
-                    int H, int n_draft, const int32_t* __restrict__ n_accept, T* __restrict__ o, bool pre16,
+decode_multi_kernel(float* __restrict__ state, const T* q, const T* k, const T* v, const float* log_alpha,
+                    const float* beta, int H, int n_draft, const int32_t* n_accept, T* __restrict__ o, bool pre16,
                     int* status) {
     constexpr int DVS = kSpecSlice;
     static_assert(DV % DVS == 0, "slice");
@@ -431,7 +429,8 @@ decode_multi_kernel(float* __restrict__ state, const T* __restrict__ q, const T*
 
 // Consecutive decode launches are chained (programmatic stream serialization): the next kernel's
 // blocks may be scheduled while the previous one drains and wait (grid_dependency_wait) before any
-// memory access.
+// memory access.  The kernel ahead may let them start while it still writes (kda_lin_*, kda_pages_* do), so no input is
+// declared const and __restrict__, which would allow the non-coherent path.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_chained(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg = {};

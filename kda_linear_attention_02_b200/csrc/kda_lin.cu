@@ -22,7 +22,7 @@ namespace {
 // (cu[0] = 0, non-decreasing, cu[N] = total); a bad table gives no items, so that the kernels behind do
 // nothing.  When all items fit one block they are ordered by length, longest first: blocks start in that order,
 // and a long sequence that started last would run on alone at the end.
-__global__ void __launch_bounds__(1024) lin_index_kernel(const int32_t* __restrict__ cu, int n_seqs, int total,
+__global__ void __launch_bounds__(1024) lin_index_kernel(const int32_t* cu, int n_seqs, int total,
                                                          int whole, int seg_len, LinHead* head, LinItem* items,
                                                          int2* multi, int* status) {
     __shared__ long long warp_sums[32];
@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(1024) lin_index_kernel(const int32_t* __restri
 // Starts of the segments: z[s] holds the end state of segment s from a zero state (segment 0: from the
 // sequence's own start), and becomes the state at the start of segment s + 1.  A thread carries four
 // elements of one state through the boundaries of its sequence.
-__global__ void __launch_bounds__(256) lin_join_kernel(const LinHead* __restrict__ head, const int2* __restrict__ multi,
-                                                       float* __restrict__ z, const float* __restrict__ zdecay, int H,
+__global__ void __launch_bounds__(256) lin_join_kernel(const LinHead* head, const int2* multi,
+                                                       float* __restrict__ z, const float* zdecay, int H,
                                                        int elems) {
     grid_launch_dependents();
     grid_dependency_wait();
@@ -121,6 +121,8 @@ __global__ void __launch_bounds__(256) lin_join_kernel(const LinHead* __restrict
     }
 }
 
+// A launch that may start while the kernel before it, which lets it, still writes: the kernels launched so wait before
+// they read, and declare nothing const and __restrict__ (which would let them read by the non-coherent path).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_chained(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg = {};

@@ -11,11 +11,9 @@ namespace kda {
 namespace {
 
 template <typename T, int DK, int DV, int NT>
-__global__ void __launch_bounds__(NT) lin_step_kernel(float* __restrict__ state, long long n_states,
-                                                      const int32_t* __restrict__ slots, int slot_stride,
-                                                      const T* __restrict__ q, const T* __restrict__ k,
-                                                      const T* __restrict__ v, const float* __restrict__ la, int la_n,
-                                                      int n, int Hqk, int H, T* __restrict__ o, int* status) {
+__global__ void __launch_bounds__(NT) lin_step_kernel(float* __restrict__ state, long long n_states, const int32_t* slots,
+                                                      int slot_stride, const T* q, const T* k, const T* v, const float* la,
+                                                      int la_n, int n, int Hqk, int H, T* __restrict__ o, int* status) {
     constexpr int CG = DV / 4, RG = NT / CG, RPT = DK / RG;
     static_assert(RG * CG == NT && RPT * RG == DK && DV <= NT && DK <= NT, "tiling");
     __shared__ float sq[DK], sk[DK];

@@ -164,8 +164,8 @@ __device__ __forceinline__ void carry_out(char* pool, int n_planes, int n_pages,
 }
 
 __global__ void __launch_bounds__(kNt) pages_move_kernel(char* pool, int n_planes, int n_pages, size_t page_bytes,
-                                                         const PlanHead* __restrict__ head,
-                                                         const int2* __restrict__ moves, bool zero) {
+                                                         const PlanHead* head,
+                                                         const int2* moves, bool zero) {
     grid_launch_dependents();
     grid_dependency_wait();
     carry_out(pool, n_planes, n_pages, page_bytes, moves, head->n_moves, zero);
@@ -315,9 +315,9 @@ __global__ void __launch_bounds__(1024) pages_fork_plan_kernel(int32_t* refs, in
 // ---------------------------------------------------------------------------------------------- free
 
 // A warp per row.  The count is taken by an exchange, so that a row named twice is freed once.
-__global__ void __launch_bounds__(kNt) pages_free_kernel(int32_t* refs, int n_pages, const int32_t* __restrict__ table,
+__global__ void __launch_bounds__(kNt) pages_free_kernel(int32_t* refs, int n_pages, const int32_t* table,
                                                          int32_t* counts, int n_rows, int max_pages,
-                                                         const int32_t* __restrict__ rows, int n, int* status) {
+                                                         const int32_t* rows, int n, int* status) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int i = blockIdx.x * (kNt / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -408,10 +408,10 @@ __global__ void __launch_bounds__(1024) pages_compact_plan_kernel(int32_t* refs,
 }
 
 __global__ void __launch_bounds__(kNt) pages_compact_kernel(char* pool, int n_planes, int n_pages, size_t page_bytes,
-                                                            const PlanHead* __restrict__ head,
-                                                            const int2* __restrict__ moves, int32_t* __restrict__ table,
-                                                            const int32_t* __restrict__ counts, int n_rows, int max_pages,
-                                                            const int32_t* __restrict__ remap, int* status) {
+                                                            const PlanHead* head,
+                                                            const int2* moves, int32_t* __restrict__ table,
+                                                            const int32_t* counts, int n_rows, int max_pages,
+                                                            const int32_t* remap, int* status) {
     grid_launch_dependents();
     grid_dependency_wait();
     const long long entries = static_cast<long long>(n_rows) * max_pages;
@@ -429,6 +429,8 @@ __global__ void __launch_bounds__(kNt) pages_compact_kernel(char* pool, int n_pl
     carry_out(pool, n_planes, n_pages, page_bytes, moves, head->n_moves, false);
 }
 
+// A launch that may start while the kernel before it, which lets it, still writes: the kernels launched so wait before
+// they read, and declare nothing const and __restrict__ (which would let them read by the non-coherent path).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_chained(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg = {};
