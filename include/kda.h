@@ -272,8 +272,8 @@ KDA_API kda_status_t kda_segment_compose(const float* transitions, const float* 
  *
  * kda_lin_chunk_fwd: the chunked form over a packed batch; cu_seqlens, initial_state, final_state,
  *   ckpt_stride, checkpoints and ckpt_cu as in kda_chunk_fwd.  Sequences of length 0 are allowed (the
- *   final state is the initial one).  o, final_state and checkpoints must not overlap each other or any
- *   input; where the sizes are known (o with q, k, v, and the two states) that is KDA_ERR_ARG.  The
+ *   final state is the initial one).  o, final_state, checkpoints and the workspace must not overlap each
+ *   other or any input; that is KDA_ERR_ARG, except for checkpoints, whose size the call does not know.  The
  *   states are accumulated in fp32 from exact products for both types; a bf16 call rounds the state that q is
  *   multiplied with once to bf16 on the way to o, and keeps the decayed scores inside a chunk to 16 bits (two
  *   bf16 parts).  q, k, v, o, states and checkpoints are 16-byte aligned, the workspace (at least
@@ -287,8 +287,8 @@ KDA_API kda_status_t kda_segment_compose(const float* transitions, const float* 
  *   rows of o stay as they were.  A slot outside n_states, or one that two rows name, is an error: those
  *   rows are left out (state and o as they were) and the status word becomes KDA_ERR_DEVICE_INPUT.
  *   n is at most 2^30, n H at most 2^31 - 1.
- *   state is 16-byte aligned; the per-token inputs need element alignment only.  o overlapping q, k or v is
- *   KDA_ERR_ARG.
+ *   state is 16-byte aligned; the per-token inputs need element alignment only.  o or
+ *   state overlapping an input or each other is KDA_ERR_ARG.
  */
 KDA_API size_t kda_lin_chunk_fwd_workspace_bytes(int64_t total_tokens, int n_seqs, int H, int dk, int dv,
                                          kda_dtype_t dtype);

@@ -432,8 +432,10 @@ def kda_lin_chunk_fwd(q, k, v, log_alpha, initial_state, cu_seqlens, o, final_st
         _same(ckpt_cu, "ckpt_cu", (n + 1,), torch.int32, q)
         if checkpoints.numel():
             ck, cc = checkpoints.data_ptr(), ckpt_cu.data_ptr()
-            for t, name in ((initial_state, "initial_state"), (final_state, "final_state")):
-                if t is not None and ck < t.data_ptr() + 4 * t.numel() and t.data_ptr() < ck + 4 * checkpoints.numel():
+            for t, name in ((initial_state, "initial_state"), (final_state, "final_state"), (o, "o"), (q, "q"), (k, "k"),
+                            (v, "v"), (log_alpha, "log_alpha"), (cu_seqlens, "cu_seqlens"), (ckpt_cu, "ckpt_cu"),
+                            (workspace, "workspace")):   # the other pairs are checked behind the binding
+                if t is not None and ck < t.data_ptr() + t.nbytes and t.data_ptr() < ck + checkpoints.nbytes:
                     raise ValueError(f"checkpoints and {name} must not overlap")
     L = _load()
     raw, back = _enter(q, "q", stream)

@@ -137,15 +137,24 @@ cudaError_t launch_chained(void (*kernel)(KArgs...), dim3 grid, dim3 block, cuda
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && x < y + nb && y < x + na;
+struct Span {
+    const void* p;
+    size_t n;
+};
+bool overlap(Span a, Span b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.n && b.n && x < y + b.n && y < x + a.n;
 }
-// o is written while other heads, which may share q and k, are still read
-bool o_overlaps(const void* o, const void* q, const void* k, const void* v, int64_t tokens, int Hqk, int H, int dk, int dv,
-                bool bf16) {
-    const size_t row = static_cast<size_t>(tokens) * (bf16 ? 2 : 4), nq = row * Hqk * dk, nv = row * H * dv;
-    return overlap(o, nv, q, nq) || overlap(o, nv, k, nq) || overlap(o, nv, v, nv);
+// Outputs are written while other heads and sequences are still read: none may lie over an input or over another output.
+template <size_t NO, size_t NI>
+bool clash(const Span (&outs)[NO], const Span (&ins)[NI]) {
+    for (size_t i = 0; i < NO; ++i) {
+        for (size_t j = i + 1; j < NO; ++j)
+            if (overlap(outs[i], outs[j])) return true;
+        for (const Span& in : ins)
+            if (overlap(outs[i], in)) return true;
+    }
+    return false;
 }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -234,13 +243,18 @@ kda_status_t kda_lin_chunk_fwd(const void* q, const void* k, const void* v, cons
     if ((log_alpha && !aligned(log_alpha, 4)) || !aligned(cu_seqlens, 4) || (ckpt_cu && !aligned(ckpt_cu, 4)))
         return KDA_ERR_ALIGN;
     if (!aligned(workspace, 256)) return KDA_ERR_ALIGN;
-    // a later segment of a sequence may be done, and the final state written, before an earlier one starts
+    // (a later segment of a sequence may be done, and the final state written, before an earlier one starts)
     const size_t st_bytes = static_cast<size_t>(n_seqs) * H * dk * dv * sizeof(float);
-    if (overlap(initial_state, st_bytes, final_state, st_bytes)) return KDA_ERR_ARG;
+    if (overlap({initial_state, st_bytes}, {final_state, st_bytes})) return KDA_ERR_ARG;
     const bool bf16 = dtype == KDA_BF16;
     const LinLayout l = layout(total_tokens, n_seqs, H, dk, dv, bf16);
     if (ws_bytes < l.total) return KDA_ERR_WORKSPACE;
-    if (o_overlaps(o, q, k, v, total_tokens, Hqk, H, dk, dv, bf16)) return KDA_ERR_ARG;
+    const size_t row = static_cast<size_t>(total_tokens) * (bf16 ? 2 : 4), nq = row * Hqk * dk, nv = row * H * dv,
+                 table = (static_cast<size_t>(n_seqs) + 1) * 4;
+    const Span outs[] = {{o, nv}, {final_state, st_bytes}, {workspace, l.total}};
+    const Span ins[] = {{q, nq}, {k, nq}, {v, nv}, {log_alpha, (la_per_token ? static_cast<size_t>(total_tokens) : 1) * H * 4},
+                        {initial_state, st_bytes}, {cu_seqlens, table}, {ckpt_stride ? ckpt_cu : nullptr, table}};
+    if (clash(outs, ins)) return KDA_ERR_ARG;
     if (static_cast<long long>(l.max_items) * H > 0x7fffffffLL) return KDA_ERR_ARG;
 
     char* ws = static_cast<char*>(workspace);
@@ -291,7 +305,11 @@ kda_status_t kda_lin_recurrent_step(float* state, int64_t n_states, const int32_
         !aligned(log_alpha, 4) || (slots && !aligned(slots, 4)))
         return KDA_ERR_ALIGN;
     if (static_cast<long long>(n) * H > 0x7fffffffLL) return KDA_ERR_ARG;
-    if (o_overlaps(o, q, k, v, n, Hqk, H, dk, dv, dtype == KDA_BF16)) return KDA_ERR_ARG;
+    const size_t nq = es * n * Hqk * dk, nv = es * n * H * dv;
+    const Span outs[] = {{o, nv}, {state, static_cast<size_t>(n_states) * H * dk * dv * 4}};
+    const Span ins[] = {{q, nq}, {k, nq}, {v, nv}, {log_alpha, (la_per_token ? static_cast<size_t>(n) : 1) * H * 4},
+                        {slots, (static_cast<size_t>(n - 1) * slot_stride + 1) * 4}};
+    if (clash(outs, ins)) return KDA_ERR_ARG;
     int* st = status_ptr();
     if (!st) return KDA_ERR_CUDA;
     return launch_lin_step(state, n_states, slots, slot_stride, q, k, v, log_alpha, la_per_token, n, Hqk, H, dk, dv,
