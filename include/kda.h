@@ -336,8 +336,9 @@ KDA_API kda_status_t kda_lin_recurrent_step(float* state, int64_t n_states, cons
  *   KDA_ERR_DEVICE_INPUT; if the free pages do not suffice, it changes nothing and the status word becomes
  *   KDA_ERR_NO_PAGES.
  * kda_pages_free: the rows' pages lose a reference each and their counts become 0 (tables and page
- *   contents stay as they were).  Naming a row twice frees it once.  A row out of range is left out, a page
- *   out of range or without references is too, and the status word becomes KDA_ERR_DEVICE_INPUT.
+ *   contents stay as they were).  Naming a row twice frees it once.  A row out of range, or whose count is
+ *   negative or above max_pages, is left out as it is, a page out of range or without references is left out too,
+ *   and the status word becomes KDA_ERR_DEVICE_INPUT.
  * kda_pages_compact: moves pages so that the n_live pages in use become pages 0..n_live-1: the k-th page in
  *   use behind the first n_live fills the k-th free page among them, the others stay.  refs and the tables
  *   follow; remap [n_pages] receives each page's new number (-1 for free pages) and n_live (device, one

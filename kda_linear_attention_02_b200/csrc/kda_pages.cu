@@ -324,8 +324,13 @@ __global__ void __launch_bounds__(kNt) pages_free_kernel(int32_t* refs, int n_pa
     if (i >= n) return;
     const int r = rows[i];
     bool bad = r < 0 || r >= n_rows;
+    // A count that no row can have stays, with the row's pages and their references.  (Counts change here by becoming 0
+    // alone, so that one which passed may at most be 0 by the time it is taken.)
     int c = 0;
-    if (!bad && lane == 0) c = atomicExch(&counts[r], 0);
+    if (!bad && lane == 0) {
+        c = atomicAdd(&counts[r], 0);
+        if (c > 0 && c <= max_pages) c = atomicExch(&counts[r], 0);
+    }
     c = __shfl_sync(0xffffffffu, c, 0);
     if (c < 0 || c > max_pages) {
         bad = true;
