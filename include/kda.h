@@ -279,7 +279,7 @@ KDA_API kda_status_t kda_segment_compose(const float* transitions, const float* 
  *   bf16 parts).  q, k, v, o, states and checkpoints are 16-byte aligned, the workspace (at least
  *   kda_lin_chunk_fwd_workspace_bytes, contents ignored) 256-byte aligned.  Results do not depend on what
  *   else is in the batch except through the split of long sequences into segments, which depends on
- *   (total_tokens, n_seqs, H) and changes the order of fp32 sums only.
+ *   total_tokens, H, dtype and, for KDA_F32, dv, and changes the order of fp32 sums only.
  *
  * kda_lin_recurrent_step: one token for each of n rows, states in place.  slots (device int32, or NULL
  *   for slots[i] = i) names the state of row i among n_states; entry i is slots[i * slot_stride], so that a

@@ -54,3 +54,29 @@ def test_scores_behind_forgotten_tokens_keep_their_bits(dk, dv, resets, reset):
     o, fs, _ = chunk(q, q, v, la, cu)
     want, b, ws, aws, _, _ = ref.run(q, q, v, la, cu, None)
     ref.check("o", o, want, (2.0 ** -16 + 2.0 ** -16 + 2.0 ** -20) * b + 2.0 ** -8 * want.abs() + 1e-30)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_results_depend_on_the_batch_through_its_tokens_alone(dtype):
+    # a long sequence that is cut into segments, at the same place in batches of as many tokens, other sequences beside it
+    H, d = 2, 64
+    g = torch.Generator(DEV)
+    g.manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    T = 100 + 3000 + 500
+    q, k, v, la = (0.1 * r(T, 1, d)).to(dtype), (0.1 * r(T, 1, d)).to(dtype), r(T, H, d).to(dtype), -0.05 * r(T, H).abs()
+    init = r(2, H, d, d)
+    got = []
+    for lens in ([100, 3000, 500], [100, 3000, 1, 0, 299, 200], [60, 40, 3000, 500]):
+        at = lens.index(3000)
+        cu = ints([sum(lens[:i]) for i in range(len(lens) + 1)])
+        s0 = torch.zeros(len(lens), H, d, d, device=DEV)
+        s0[at] = init[0]
+        # what the others hold must not matter either
+        rest = torch.cat([torch.arange(100), torch.arange(3100, T)]).to(DEV)
+        x = v.clone()
+        x[rest] = r(rest.numel(), H, d).to(dtype)
+        o, fs, _ = chunk(q, k, x, la, cu, s0)
+        got.append((o[100:3100], fs[at]))
+    for o, fs in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(fs, got[0][1])
