@@ -271,12 +271,13 @@ KDA_API kda_status_t kda_segment_compose(const float* transitions, const float* 
  * the token's chunk of KDA_CHUNK tokens on; other sequences and heads, and earlier chunks, are untouched.
  *
  * kda_lin_chunk_fwd: the chunked form over a packed batch; cu_seqlens, initial_state, final_state,
- *   ckpt_stride, checkpoints and ckpt_cu as in kda_chunk_fwd.  Sequences of length 0 are allowed (the
- *   final state is the initial one).  o, final_state, checkpoints and the workspace must not overlap each
- *   other or any input; that is KDA_ERR_ARG, except for checkpoints, whose size the call does not know.  The
- *   states are accumulated in fp32 from exact products for both types; a bf16 call rounds the state that q is
- *   multiplied with once to bf16 on the way to o, and keeps the decayed scores inside a chunk to 16 bits (two
- *   bf16 parts).  q, k, v, o, states and checkpoints are 16-byte aligned, the workspace (at least
+ *   ckpt_stride, checkpoints and ckpt_cu as in kda_chunk_fwd; checkpoints may be NULL where ckpt_cu has no places
+ *   (a checkpoint without a place is left out, and the status word becomes KDA_ERR_DEVICE_INPUT).  Sequences
+ *   of length 0 are allowed (the final state is the initial one).  o, final_state, checkpoints and the workspace
+ *   must not overlap each other or any input; that is KDA_ERR_ARG, except for checkpoints, whose size the call
+ *   does not know.  The states are accumulated in fp32 from exact products for both types; a bf16 call rounds
+ *   the state that q is multiplied with once to bf16 on the way to o, and keeps the decayed scores inside a chunk
+ *   to 16 bits (two bf16 parts).  q, k, v, o, states and checkpoints are 16-byte aligned, the workspace (at least
  *   kda_lin_chunk_fwd_workspace_bytes, contents ignored) 256-byte aligned.  Results do not depend on what
  *   else is in the batch except through the split of long sequences into segments, which depends on
  *   total_tokens, H, dtype and, for KDA_F32, dv, and changes the order of fp32 sums only.

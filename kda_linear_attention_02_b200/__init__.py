@@ -405,7 +405,8 @@ def kda_lin_chunk_fwd(q, k, v, log_alpha, initial_state, cu_seqlens, o, final_st
     S_t = a_t S_{t-1} + k_t v_t^T, o_t = S_t^T q_t, a_t = exp(log_alpha_t), one decay per head.  q, k
     [T,Hqk,dk] (bf16 or fp32; H a multiple of Hqk); v, o [T,H,dv]; log_alpha fp32 [T,H], or [H] for a constant
     of each head; cu_seqlens int32 [N+1] (device); initial_state / final_state [N,H,dk,dv] fp32 or None;
-    checkpoints, ckpt_cu and workspace as in kda_chunk_fwd.  Outputs are written in place.
+    checkpoints, ckpt_cu and workspace as in kda_chunk_fwd; an empty checkpoints tensor has no places, and a
+    checkpoint without a place is reported by kda_get_device_status.  Outputs are written in place.
     """
     _need(q, "q")
     if q.dim() != 3 or v is None or v.dim() != 3 or cu_seqlens is None:
@@ -430,8 +431,9 @@ def kda_lin_chunk_fwd(q, k, v, log_alpha, initial_state, cu_seqlens, o, final_st
         if checkpoints.dim() != 4 or checkpoints.shape[1:] != (H, dk, dv):
             raise ValueError("checkpoints must be [n_ckpt, H, dk, dv]")
         _same(ckpt_cu, "ckpt_cu", (n + 1,), torch.int32, q)
-        if checkpoints.numel():
-            ck, cc = checkpoints.data_ptr(), ckpt_cu.data_ptr()
+        cc = ckpt_cu.data_ptr()
+        if checkpoints.numel():     # else a null pointer: no places, and a checkpoint that falls due is reported
+            ck = checkpoints.data_ptr()
             for t, name in ((initial_state, "initial_state"), (final_state, "final_state"), (o, "o"), (q, "q"), (k, "k"),
                             (v, "v"), (log_alpha, "log_alpha"), (cu_seqlens, "cu_seqlens"), (ckpt_cu, "ckpt_cu"),
                             (workspace, "workspace")):   # the other pairs are checked behind the binding
@@ -446,7 +448,7 @@ def kda_lin_chunk_fwd(q, k, v, log_alpha, initial_state, cu_seqlens, o, final_st
             _need(workspace, "workspace", None, torch.uint8, q.device)
         st = L.kda_lin_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), per_token,
                                  _ptr(initial_state), cu_seqlens.data_ptr(), n, T, Hqk, H, dk, dv, dt,
-                                 int(ckpt_stride) if ck else 0, o.data_ptr(), _ptr(final_state), ck, cc,
+                                 int(ckpt_stride), o.data_ptr(), _ptr(final_state), ck, cc,
                                  workspace.data_ptr(), workspace.numel(), raw)
     finally:
         if back is not None:

@@ -233,7 +233,7 @@ kda_status_t kda_lin_chunk_fwd(const void* q, const void* k, const void* v, cons
     if (total_tokens > 0x7fffffffLL) return KDA_ERR_ARG;   // cu_seqlens is int32
     if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_ARG;
     if (!dims_ok(dk, dv)) return KDA_ERR_UNSUPPORTED;
-    if (ckpt_stride > 0 && (ckpt_stride % kChunk != 0 || !checkpoints || !ckpt_cu)) return KDA_ERR_ARG;
+    if (ckpt_stride > 0 && (ckpt_stride % kChunk != 0 || !ckpt_cu)) return KDA_ERR_ARG;
     if (n_seqs == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_ARG;
     if (!cu_seqlens || !workspace) return KDA_ERR_ARG;
     if (total_tokens > 0 && (!q || !k || !v || !log_alpha || !o)) return KDA_ERR_ARG;

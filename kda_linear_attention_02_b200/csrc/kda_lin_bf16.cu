@@ -844,7 +844,7 @@ lin_bf16_kernel(const LinArgs a, const __grid_constant__ CUtensorMap mq, const _
             if (!BOUNDARY && a.ckpt_stride) {
                 const int first = a.ckpt_cu[it.seq] + it.pos / a.ckpt_stride;
                 to_ck = a.ckpt_stride - it.pos % a.ckpt_stride;
-                ck_room = first >= 0 ? a.ckpt_cu[it.seq + 1] - first : 0;
+                ck_room = first >= 0 && a.checkpoints ? a.ckpt_cu[it.seq + 1] - first : 0;
                 ck = a.checkpoints + (static_cast<long long>(first) * a.H + h) * (DK * DV);
             }
             // A chunk's checkpoint and the segment's end are written once the next chunk's products have their copy of

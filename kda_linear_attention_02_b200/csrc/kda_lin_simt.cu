@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kNt + 32) lin_simt_kernel(const LinArgs a) {
             to_ck -= kC;
             if (to_ck == 0 && n == kC) {
                 to_ck = a.ckpt_stride;
-                if (ck >= 0 && ck < a.ckpt_cu[it.seq + 1])
+                if (ck >= 0 && a.checkpoints && ck < a.ckpt_cu[it.seq + 1])
                     store_state(a.checkpoints + (static_cast<size_t>(ck) * a.H + h) * st_elems);
                 else if (t == 0)
                     set_status(a.status, KDA_ERR_DEVICE_INPUT);
