@@ -345,8 +345,9 @@ def kda_lin_chunk_fwd_workspace_bytes(total_tokens, n_seqs, H, dk, dv, dtype=KDA
 
 # The calls below are a few microseconds on the device when the work is small, so their host side is kept short:
 # checks that cost little when they pass, device indices instead of device objects, sizes remembered by their numbers.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
+# (The two short ways are private to torch; where one is missing the public way does the same, more slowly.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _enter(t: torch.Tensor, name: str, stream):
