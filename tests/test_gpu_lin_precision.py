@@ -80,3 +80,58 @@ def test_results_depend_on_the_batch_through_its_tokens_alone(dtype):
         got.append((o[100:3100], fs[at]))
     for o, fs in got[1:]:
         assert torch.equal(o, got[0][0]) and torch.equal(fs, got[0][1])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("T,stride", [(64, 0), (61, 0), (330, 64), (3000, 512)], ids=["chunk", "ragged", "chunks", "segments"])
+def test_what_a_token_leaves_in_the_state_is_exact_to_fp32(dtype, dk, dv, T, stride):
+    # One token of each head has a value, so that the state is the single product w k v, w the decay up to its chunk's end
+    # (nothing decays in other chunks, whose factors are exactly 1, and adding zeros is exact).  With w exact to
+    # 2^-22 (the exponential) and the logarithms' sum to a rounding of at most 4 in magnitude (4 x 2^-24), two roundings
+    # of the products and one of the sum, that is 2^-22 + 7 x 2^-24 of the value: bf16 has to have all of w v's 24 bits.
+    H, n = 16, 3
+    g = torch.Generator(DEV)
+    g.manual_seed(T + dk + dv)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    q, k, v = (r(n * T, 1, dk)).to(dtype), (r(n * T, 1, dk)).to(dtype), torch.zeros(n * T, H, dv, dtype=dtype, device=DEV)
+    la, cu = torch.zeros(n * T, H, device=DEV), ints([0, T, 2 * T, 3 * T])
+    for i in range(n):
+        for h in range(H):
+            j = ((i * H + h) * 1009 + h) % T if i else min(T - 1, 4 * h)           # all over; in the first, a chunk's places
+            c = j - j % 64
+            e = min(T, c + 64)
+            v[i * T + j, h] = r(dv).to(dtype)
+            la[i * T + c:i * T + e, h] = -0.06 * torch.rand(e - c, generator=g, device=DEV)
+    _, fs, ck = chunk(q, k, v, la, cu, stride=stride)
+    _, _, want, _, wck, _ = ref.run(q, k, v, la, cu, None, stride)
+    bound = 2.0 ** -22 + 7 * 2.0 ** -24
+    ref.check("final_state", fs, want, bound * want.abs())
+    if stride:
+        # (the checkpoint at a chunk's end, and those behind it)
+        ref.check("checkpoints", ck, wck, bound * wck.abs())
+    assert (want != 0).any(dim=(2, 3)).all()
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("decay", [-6.0, -1.0, 1.0])
+def test_scores_keep_their_second_part_in_every_chunk(dk, dv, decay):
+    # Every chunk's first token forgets what was before, so that o is made of its chunk's scores alone: in every chunk,
+    # of sequences of several and of pairs that a CTA takes one behind another.  Scores: two bf16 parts (2^-16), the
+    # exponent (2^-16, above), fp32 sums; then o's own rounding.
+    lens = [64, 130, 1, 200, 63, 65, 128, 7] * 3
+    T, H = sum(lens), 16
+    g = torch.Generator(DEV)
+    g.manual_seed(dk + dv)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    unit = lambda x: (x / x.norm(dim=-1, keepdim=True)).to(BF)  # noqa: E731
+    q, k, v, la = unit(r(T, 2, dk)), unit(r(T, 2, dk)), r(T, H, dv).to(BF), -torch.exp(r(T, H) + decay)
+    starts = [sum(lens[:i]) for i in range(len(lens) + 1)]
+    for a, b in zip(starts, starts[1:]):
+        la[a:b:64] = float("-inf")
+    o, _, _ = chunk(q, k, v, la, ints(starts), 0.3 * r(len(lens), H, dk, dv))
+    want, b = ref.run(q, k, v, la, ints(starts), None)[:2]
+    tol = (2.0 ** -16 + 2.0 ** -16 + ref.f32_factor(64, dk)) * b * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs() + 1e-30
+    ref.check("o", o, want, tol)
+    # with one part, the half step of 2^-8 that this would leave in each score shows where values cancel
+    assert float((2.0 ** -8 * b / tol).max()) > 20
