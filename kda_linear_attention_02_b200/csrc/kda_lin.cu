@@ -259,7 +259,7 @@ kda_status_t kda_lin_chunk_fwd(const void* q, const void* k, const void* v, cons
 
     char* ws = static_cast<char*>(workspace);
     LinArgs a{};
-    a.q = q; a.k = k; a.v = v; a.la = log_alpha; a.la_t = la_per_token ? H : 0; a.la_h = 1;
+    a.q = q; a.k = k; a.v = v; a.la = log_alpha; a.la_t = la_per_token ? H : 0;
     a.initial_state = initial_state; a.cu_seqlens = cu_seqlens; a.n_seqs = n_seqs; a.total_tokens = total_tokens;
     a.Hqk = Hqk; a.H = H; a.dk = dk; a.dv = dv; a.ckpt_stride = ckpt_stride; a.o = o; a.final_state = final_state;
     a.checkpoints = checkpoints; a.ckpt_cu = ckpt_cu;

@@ -39,7 +39,7 @@ struct LinArgs {
     const void* k;
     const void* v;
     const float* la;
-    int la_t, la_h;              // log_alpha of (token, head) is la[token * la_t + head * la_h]
+    int la_t;                    // log_alpha of (token, head) is la[token * la_t + head]
     const float* initial_state;
     const int32_t* cu_seqlens;
     int n_seqs;

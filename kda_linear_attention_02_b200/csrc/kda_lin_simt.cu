@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kNt + 32) lin_simt_kernel(const LinArgs a) {
     if (t >= kNt) {
         // ---------------- decays of chunk c into buffer (c / C) % 2, one chunk ahead of the other warps
         const int lane = t & 31;
-        const float* la = a.la + static_cast<size_t>(h) * a.la_h;
+        const float* la = a.la + h;
         auto load = [&](int c) {
             return c + lane < it.n ? fmaxf(la[(static_cast<size_t>(it.t0) + c + lane) * a.la_t], kLinLogMin) : 0.f;
         };
