@@ -260,7 +260,7 @@ KDA_API kda_status_t kda_segment_compose(const float* transitions, const float* 
  *
  * There is no scale on q and no floor under the decay: a_t may be any value in [0, 1].  log_alpha below
  * -120, minus infinity and NaN among it, is a decay of 0 (exp(-120) is 0 in fp32): the state is forgotten
- * before token t is added.  log_alpha > 0 is outside the contract.
+ * before token t is added (a finite one: 0 times infinity or NaN is NaN).  log_alpha > 0 is outside the contract.
  *
  *   q, k       [T_tot, Hqk, dk]; H must be a multiple of Hqk, and head h reads q and k of head h Hqk / H
  *   v, o       [T_tot, H, dv]

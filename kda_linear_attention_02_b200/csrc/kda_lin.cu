@@ -166,7 +166,10 @@ bool dims_ok(int dk, int dv) { return (dk == 64 || dk == 128) && (dv == 64 || dv
 // once and what is left over fills the rest, but at least `least` tokens, below which a segment's set-up and the
 // extra pass cost more than they give.  Measured, bf16, segments of half a share and of a share, each with 1/32
 // more: 32768 tokens x 4 heads 110 and 76 us, 16384 x 16 heads 112 and 99 us, 3 x 10000 x 16 heads 174 and 158 us;
-// of a share without more, or with 1/16: up to 10 % slower.  fp32, whose blocks share an SM, keeps half a share.
+// of a share without more, or with 1/16: up to 10 % slower.
+// fp32 keeps half a share: at dk = 64 two blocks share an SM (half and whole: 16384 tokens x 4 heads 133 and 223 us,
+// 4 x 4096 x 8 heads 221 and 415); at dk = 128 one fits, and the choice matters little (392 and 376, 585 and 584 us;
+// dv = 64, 3 heads of 5 x 3000: 163 and 172).
 struct SegRule {
     int whole, len;
 };

@@ -8,13 +8,17 @@
 //     o_t      = e^{g_t} (S^T q_t)  +  sum_j P_tj v_j             (O1 = Sb Q^T, O2 = V^T P^T)
 //     S^T     <- e^{g_C} S^T + sum_j (e^{g_C - g_j} v_j) k_j^T    (Z = W K, W_j = e^{g_C - g_j} v_j)
 //
-// S^T stays in fp32 registers (thread = channel of v, register = channel of k); its bf16 copy Sb goes to
-// tensor memory as O1's A operand, in the lane layout the registers already have, and W is an A operand there
-// too.  On the way to o the copy of S is rounded once, channel by channel, and such errors average out over the
-// sum.  P's would not: one P_tj weighs all of v_j, so with a single bf16 part an output that one token dominates
-// would be off by up to 2^-8 in every channel; a second part leaves 2^-16 and costs 2 % of the time.  What reaches
-// the state is not rounded: k and v are bf16 already, and W goes in as four bf16 parts that add up to w v to 24 bits, so Z is an fp32 sum
-// of exact products.  With w = w1 + w2 + w3 in bf16 parts, packed bf16 FMAs give them two tokens at a time,
+// S^T stays in fp32 registers (thread = channel of v, register = channel of k); its bf16 copy Sb goes to tensor
+// memory as O1's A operand, in the lane layout the registers already have, and W is an A operand there too.  On the
+// way to o the copy of S is rounded once, channel by channel, and such errors average out over the sum: o is off by
+// 0.0018 to 0.0021 of its norm, 0.0017 of it o's own rounding.  (With a second part of the copy that is all of it,
+// but tensor memory has room for both parts of 64 channels at a time: 4 x 4096 x 32 heads 157 -> 198 us, 32768 x 32
+// heads 411 -> 489 us.)  P's would not: one P_tj weighs all of v_j, so with a single bf16 part an output that one
+// token dominates would be off by up to 2^-8 in every channel; a second part leaves 2^-16 and costs 2 % of the
+// time.  For the same 16 bits the exponents g_t - g_j are differences of numbers in two parts (Log2, below), 1 to 4
+// % of the time.  What reaches the state is not rounded: k and v are bf16 already, and W goes in as four bf16 parts
+// that add up to w v to 24 bits, so Z is an fp32 sum of exact products.  With w = w1 + w2 + w3 in bf16 parts,
+// packed bf16 FMAs give them two tokens at a time,
 //     h = rn(w1 v),  -e = h - w1 v (exact: eight bits are left),  m = rn(w2 v),  -l = rn((m - w2 v) - w3 v),
 // five instructions a pair (splitting the fp32 products w v takes seventeen); the MMAs negate -e and
 // -l.  Z starts from zero in every chunk and joins S by one rounded FMA: an accumulator that lived on in tensor
@@ -27,8 +31,8 @@
 // an issuer (all MMAs, in an order that keeps Z of one chunk ahead of the scores of the next), two warps for
 // P, four that split W, four that write o, four that hold the state.
 //
-// What bounds it (4 x 4096 tokens x 32 heads of 128, 614 MB): 149-157 us = 3.9-4.1 TB/s, 129 us of it this kernel.  A
-// chunk takes 2900 cycles: the products about 2050 of the tensor pipe (59 % busy), with shared memory and W's warps
+// What bounds it (4 x 4096 tokens x 32 heads of 128, 614 MB): 147-158 us = 3.9-4.2 TB/s, 135 us of it this kernel.  A
+// chunk takes 2900 cycles: the products about 2050 of the tensor pipe (57 % busy), with shared memory and W's warps
 // close behind.  M = 128 for the channels of v leaves one product shape for all sizes of dv; chunks of 64 keep P at
 // one N = 64 operand, and three 48 KB stages beside it in shared memory.  Before: bf16 P in one part 147 us, W as
 // three parts of the fp32 products 201 us, fp32 units 4840 us.

@@ -15,7 +15,9 @@
 // copied (cp.async) and a ninth warp forms the next one's decays.
 //
 // 3 sequences of up to 256 tokens x 2 heads of 64: 29 us for a call, 18 of them in the full pass: a chain of chunks on
-// 40 blocks.  4 x 4096 tokens x 8 heads of 128: 581 us, bound by the shared-memory reads (one output a thread: 1223).
+// 40 blocks.  4 x 4096 tokens x 8 heads of 128: 581 us, bound by the
+// shared-memory reads of one block of nine warps on an SM, all of which wait at its barriers (one output a thread: 1223).
+// Both figures with segments of half a share of the SMs (see segment_rule).
 #include "kda_device.cuh"
 #include "kda_lin.h"
 
@@ -26,7 +28,7 @@ namespace {
 constexpr int kC = 32, kDvs = 32, kNt = 256;   // and a warp for the decays
 constexpr int kPart = kDvs + 8;                // pitch that keeps four rows of eight columns in different banks
 
-// (two blocks of DK = 128 fit an SM)
+// DK = 64: 77 KB, two blocks on an SM (96 registers x 288 threads); DK = 128: 118 KB, one.
 template <int DK>
 struct SimtSmem {
     float q[2][kC][DK + 4], k[2][kC][DK + 4], v[2][kC][kDvs];
