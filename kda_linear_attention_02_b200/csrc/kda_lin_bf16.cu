@@ -31,7 +31,7 @@
 // an issuer (all MMAs, in an order that keeps Z of one chunk ahead of the scores of the next), two warps for
 // P, four that split W, four that write o, four that hold the state.
 //
-// What bounds it (4 x 4096 tokens x 32 heads of 128, 614 MB): 147-158 us = 3.9-4.2 TB/s, 135 us of it this kernel.  A
+// What bounds it (4 x 4096 tokens x 32 heads of 128, 614 MB): 147-160 us = 3.8-4.2 TB/s, 135 us of it this kernel.  A
 // chunk takes 2900 cycles: the products about 2050 of the tensor pipe (57 % busy), with shared memory and W's warps
 // close behind.  M = 128 for the channels of v leaves one product shape for all sizes of dv; chunks of 64 keep P at
 // one N = 64 operand, and three 48 KB stages beside it in shared memory.  Before: bf16 P in one part 147 us, W as
